@@ -10,7 +10,8 @@ binding raises.
 Entry points (same names as the C ABI, without the ``instagen_`` prefix):
 ``cluster``, ``permutation``, ``gather``, ``select_sample``, ``attention``,
 ``forward``, ``forward_host`` plus ``make_params``, ``exact_budget``, ``sample_budget``,
-``workspace_size``, ``forward_layout`` and ``device_status``.
+``workspace_size``, ``forward_layout`` and ``device_status``; for language
+models ``prompt_attention``, ``key_weights``, ``prefix_attention`` and ``evict``.
 """
 from __future__ import annotations
 
@@ -49,6 +50,19 @@ class ForwardLayout(ctypes.Structure):
         "exact_groups", "counts", "sample_pos", "sample_bias", "votes", "pq_ws", "cluster_ws", "total")]
 
 
+class PromptParams(ctypes.Structure):
+    """Mirror of ``instagen_prompt_params``."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("nseq", "Hq", "Hkv", "d", "Tq", "Tk", "dtype", "causal")] + \
+        [("softmax_scale", ctypes.c_float)] + \
+        [(n, ctypes.c_int64) for n in ("q_tok", "q_head", "k_tok", "k_head", "v_tok", "v_head", "o_tok", "o_head")]
+
+
+class CacheParams(ctypes.Structure):
+    """Mirror of ``instagen_cache_params``."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "Hq", "Hkv", "d", "P", "cap", "dtype")] + \
+        [("softmax_scale", ctypes.c_float), ("q_seq", ctypes.c_int64), ("prefix_head", ctypes.c_int64)]
+
+
 _lib = None
 _SYMBOLS = ("instagen_exact_budget", "instagen_sample_budget", "instagen_workspace_size",
             "instagen_cluster_workspace_size", "instagen_error_string", "instagen_device_status",
@@ -56,7 +70,10 @@ _SYMBOLS = ("instagen_exact_budget", "instagen_sample_budget", "instagen_workspa
             "instagen_attention", "instagen_forward", "instagen_forward_layout_get",
             "instagen_cluster_static", "instagen_forward_host_workspace_size", "instagen_forward_host",
             "instagen_forward_init", "instagen_pq_votes_workspace_size", "instagen_pq_votes",
-            "instagen_select_sample_votes")
+            "instagen_select_sample_votes", "instagen_prompt_attention_workspace_size", "instagen_prompt_attention",
+            "instagen_key_weights_workspace_size", "instagen_key_weights",
+            "instagen_prefix_attention_workspace_size", "instagen_prefix_attention",
+            "instagen_evict_workspace_size", "instagen_evict")
 
 
 def lib():
@@ -91,6 +108,17 @@ def lib():
         "instagen_pq_votes": (ctypes.c_int, [PP, PP, PP, PP, PP, PP, P, PP, PP, sz, vp]),
         "instagen_select_sample_votes": (ctypes.c_int, [PP, PP, PP, PP, P, PP, PP, PP, PP, vp]),
     }
+    PR, PC = ctypes.POINTER(PromptParams), ctypes.POINTER(CacheParams)
+    sig.update({
+        "instagen_prompt_attention_workspace_size": (sz, [PR]),
+        "instagen_prompt_attention": (ctypes.c_int, [PP, PP, PP, PP, PP, PR, PP, PP, PP, sz, vp]),
+        "instagen_key_weights_workspace_size": (sz, [PR]),
+        "instagen_key_weights": (ctypes.c_int, [PP, PP, PP, PP, PP, PR, PP, PP, sz, vp]),
+        "instagen_prefix_attention_workspace_size": (sz, [PC, i32]),
+        "instagen_prefix_attention": (ctypes.c_int, [PP, PP, PP, PP, PP, PP, PC, PP, PP, PP, PP, sz, vp]),
+        "instagen_evict_workspace_size": (sz, [PC, i32]),
+        "instagen_evict": (ctypes.c_int, [PP, PP, PP, PP, PP, PC, i32, i32, PP, PP, PP, PP, PP, i32, PP, sz, vp]),
+    })
     for name, (res, args) in sig.items():
         f = getattr(L, name)
         f.restype = res
@@ -389,3 +417,6 @@ def forward_intermediates(workspace: torch.Tensor, p: Params) -> dict:
         sample_bias=view(L.sample_bias, B * H * Cq * m, torch.float32, (B, H, Cq, m)),
         **({"votes": view(L.votes, B * H * Cq * Ck, torch.int32, (B, H, Cq, Ck))} if p.selection == PQ_VOTE else {}),
     )
+
+
+from .serve import evict, key_weights, prefix_attention, prompt_attention  # noqa: E402,F401

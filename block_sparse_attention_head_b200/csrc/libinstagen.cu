@@ -7,3 +7,7 @@
 #include "attention.cu"
 #include "api.cu"
 #include "cluster_static.cu"
+#include "prompt.cu"
+#include "step.cu"
+#include "evict.cu"
+#include "serve_api.cu"

@@ -342,6 +342,128 @@ typedef struct {
 
 int instagen_forward_layout_get(const instagen_params* p, instagen_forward_layout* out);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Attention of a language model: a whole prompt, one generated token per
+ * sequence, and a cache that keeps the keys that matter.  No counterpart on
+ * the method's pages.  Dense (every visible key is attended), with grouped
+ * heads: query head h reads key/value head h / G, G = Hq / Hkv.  Together:
+ * instagen_prompt_attention gives a prompt's outputs and its rows' log-sum-
+ * exp, instagen_key_weights from them the attention mass of every key,
+ * instagen_evict the keys worth keeping, instagen_prefix_attention the next
+ * token's attention over them (adding its own weights), instagen_evict again
+ * when the cache is full.
+ *
+ * Shared by these entry points: 16-bit tensors are all bf16 or all fp16
+ * (dtype); dots and softmax statistics are fp32; the probabilities that
+ * multiply V are rounded to the tensors' type (each rounding at most half a
+ * step of it), O once at the end; lse is the natural log of the sum of
+ * exp(softmax_scale * q.k) and -inf for a row that sees no key, whose O is 0.
+ * Contents of K and V rows behind a sequence's end (or past a cache's length)
+ * never matter, NaN included; values a sequence's own rows hold must be
+ * finite (a non-finite V row may reach earlier rows of the same sequence
+ * through a zero probability).  Results do not depend on timing: no atomics
+ * on floats.  Pointers to 16-bit tensors, O and lse must be 16-byte aligned.
+ * Workspaces are scratch: 256-byte aligned, no contents kept; calls that may
+ * overlap on the GPU (two streams, two captured graphs) need one each.  A
+ * size function returns 0 for invalid parameters and at least 256 otherwise.
+ */
+typedef enum { IG_BF16 = 0, IG_F16 = 1 } instagen_dtype;
+
+typedef struct {
+  int32_t nseq;              /* packed sequences, 1 .. 2^20                           */
+  int32_t Hq, Hkv, d;        /* heads (Hkv divides Hq); d in {64, 128}                */
+  int32_t Tq, Tk;            /* rows of Q and of K, V: >= every end in cu_q / cu_k    */
+  int32_t dtype;             /* instagen_dtype of Q, K, V, O                          */
+  int32_t causal;            /* 1: query i of a sequence sees its keys j <= i + n_k - n_q
+                                (the last query sees all); 0: every query sees all    */
+  float softmax_scale;       /* logit scale > 0                                       */
+  /* strides in elements, multiples of 8: from a token to the next and from a
+   * head to the next; the d elements of a row are contiguous, rows of one
+   * tensor do not overlap (a stride of a dimension of size 1 is not used)    */
+  int64_t q_tok, q_head, k_tok, k_head, v_tok, v_head, o_tok, o_head;
+} instagen_prompt_params;
+
+/*
+ * Attention over whole prompts, packed: sequence s has the query rows
+ * [cu_q[s], cu_q[s+1]) and the key rows [cu_k[s], cu_k[s+1]).  n_q and n_k
+ * may differ (the last chunk of a prompt against all its keys) and either may
+ * be 0; with causal set and n_k < n_q the first n_q - n_k rows see nothing.
+ *   Q [Tq, Hq, d], K and V [Tk, Hkv, d], strided; O [Tq, Hq, d], strided.
+ *   cu_q, cu_k [nseq+1] int32 on the device, ascending, within [0, Tq] and
+ *   [0, Tk] (anything else is clamped and an IG_ERR_DEVICE_CHECK).
+ *   lse [Hq, Tq] fp32 out, contiguous (may be NULL).
+ * Rows of O and lse that belong to no sequence are left as they were.
+ */
+size_t instagen_prompt_attention_workspace_size(const instagen_prompt_params* p);
+int instagen_prompt_attention(const void* Q, const void* K, const void* V, const int32_t* cu_q, const int32_t* cu_k,
+                              const instagen_prompt_params* p, void* O, float* lse, void* ws, size_t ws_bytes,
+                              void* stream);
+
+/*
+ * Attention mass of every key: weights[hkv, j] += the sum over the G heads
+ * and the queries i that see key j of exp(softmax_scale * q_i.k_j - lse_i),
+ * lse as instagen_prompt_attention gave it (rows with lse = -inf add
+ * nothing).  The queries may be fewer than those of the prompt (cu_q of the
+ * last w queries of every sequence: their mass alone).
+ *   Arguments as above (v_*, o_* strides unused); weights [Hkv, Tk] fp32,
+ *   contiguous; entries of keys that belong to no sequence stay as they were.
+ */
+size_t instagen_key_weights_workspace_size(const instagen_prompt_params* p);
+int instagen_key_weights(const void* Q, const void* K, const float* lse, const int32_t* cu_q, const int32_t* cu_k,
+                         const instagen_prompt_params* p, float* weights, void* ws, size_t ws_bytes, void* stream);
+
+typedef struct {
+  int32_t B, Hq, Hkv, d;     /* sequences, heads (Hkv divides Hq), d in {64, 128}     */
+  int32_t P;                 /* keys of the prefix that all sequences share, >= 0     */
+  int32_t cap;               /* slots of each sequence's own cache, >= 0              */
+  int32_t dtype;             /* instagen_dtype                                        */
+  float softmax_scale;       /* logit scale > 0 (instagen_evict: not used)            */
+  int64_t q_seq;             /* Q: elements from a sequence to the next (its Hq rows
+                                are contiguous), a multiple of 8                      */
+  int64_t prefix_head;       /* Kp, Vp: elements from a head to the next (rows are
+                                contiguous), a multiple of 8                          */
+} instagen_cache_params;
+
+/*
+ * Attention of one new token per sequence over a shared prefix and the
+ * sequence's own cache.  The prefix is read once for the whole batch.
+ *   Q [B, Hq, d]; Kp, Vp [Hkv, P, d] (may be NULL when P = 0); Kc, Vc
+ *   [B, Hkv, cap, d] contiguous (may be NULL when cap = 0); lens [B] int32 on
+ *   the device: live slots of each cache, in [0, cap] (anything else is
+ *   clamped and an IG_ERR_DEVICE_CHECK).
+ *   O [B, Hq, d] contiguous; lse [B, Hq] fp32 (may be NULL).
+ *   weights [B, Hkv, cap] fp32 or NULL: the token's attention weight on every
+ *   live slot of its own cache, summed over the G heads, is added.
+ */
+size_t instagen_prefix_attention_workspace_size(const instagen_cache_params* p, int32_t with_weights);
+int instagen_prefix_attention(const void* Q, const void* Kp, const void* Vp, const void* Kc, const void* Vc,
+                              const int32_t* lens, const instagen_cache_params* p, void* O, float* lse,
+                              float* weights, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Eviction from the caches by accumulated attention weight.  Of the n =
+ * lens[b] live slots of each (sequence, head), min(n, budget) stay: first the
+ * most recent ones (pos > largest pos - recent), then those of the largest
+ * weight (NaN below every number), ties to the lower slot.  Kept slots below
+ * `budget` stay where they are; the kept slots from `budget` on move into the
+ * freed ones below it, both in ascending order.  So nothing is read and
+ * written by the same call and few rows move when few are evicted; a slot's
+ * position is what pos says, not its index.
+ *   K, V [B, Hkv, cap, d], weights [B, Hkv, cap] fp32, pos [B, Hkv, cap] int32
+ *   (token positions), lens [B] int32 (clamped as above).
+ *   Outputs: all five pointers equal to the inputs and cap_out = cap (in
+ *   place: only the moving rows are touched), or all five distinct buffers
+ *   with cap_out slots per head (the kept rows are copied; a large prompt
+ *   cache into a small one).  lens_out = min(n, budget); output slots from
+ *   there on stay as they were.  1 <= budget <= cap_out, recent >= 0.
+ */
+size_t instagen_evict_workspace_size(const instagen_cache_params* p, int32_t budget);
+int instagen_evict(const void* K, const void* V, const float* weights, const int32_t* pos, const int32_t* lens,
+                   const instagen_cache_params* p, int32_t budget, int32_t recent, void* K_out, void* V_out,
+                   float* weights_out, int32_t* pos_out, int32_t* lens_out, int32_t cap_out, void* ws,
+                   size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
