@@ -8,6 +8,7 @@
 #include "api.cu"
 #include "cluster_static.cu"
 #include "prompt.cu"
+#include "key_weights.cu"
 #include "step.cu"
 #include "evict.cu"
 #include "serve_api.cu"

@@ -1,135 +1,734 @@
-// Attention over packed prompts (instagen_prompt_attention) and the attention
-// mass of their keys (instagen_key_weights).  Simple form: one warp per query
-// row, or per key, with the d elements of a row spread over the lanes.
+// Dense attention on the tensor cores, for packed prompts and for a prefix
+// that a batch shares (instagen_prompt_attention, instagen_prefix_attention).
+//
+// A key/value head serves the G query heads of its group, so the query rows
+// of a sequence are numbered r = token * G + head of the group, and a CTA
+// takes 256 consecutive rows of one (sequence, key/value head) in two tiles of
+// 128 over the same key tiles: every K and V tile brought on chip serves all
+// the heads of the group.  Per key tile j and row tile t:
+//   S_t = Q_t K_j^T     tcgen05 (M=128, N=128), fp32 in TMEM
+//   P_t = 2^(c S_t - m_t), rounded to the tensors' type, into S_t's columns
+//   O_t += P_t V_j      tcgen05 with A (P_t) read from TMEM
+// with c = softmax_scale log2(e) and m_t the running maximum, raised only when
+// it grows by more than 8 (P <= 256), which keeps rescaling O rare.  The two
+// chains run independently (two softmax warpgroups, one thread per row; two MMA
+// warps), so one chain's exponentials overlap the other's MMAs.  A CTA with one
+// row tile gives chain 0 the even and chain 1 the odd key tiles and merges the
+// two partial softmaxes at the end.
+//
+// Bound: 4 * 512 tensor cycles per key tile and CTA (d = 128) against 2 * 1024
+// of exponentials on the MUFU; a quarter of the exponentials of unmasked tiles
+// are therefore evaluated on the FMA pipe.
+//
+// Few rows, many keys: nsplit CTAs share a row tile pair, each over its part
+// of the key tiles, and write normalised partial outputs with their log-sum-
+// exp, which combine_kernel joins.
+//
+// Masks: a row sees a prefix of its sequence's keys (causal or not), so a tile
+// is full, cut, or skipped.  Keys behind the sequence's end are never seen; V
+// rows there may hold anything, so the last tile's are zeroed on chip (0 * NaN
+// would reach every row).
 #include "serve.cuh"
+
+#include <type_traits>
 
 namespace ig {
 
 namespace {
-constexpr int kRowThreads = 128;
+constexpr int kTcThreads = 384;
+constexpr int kTcRows = 256;        // query rows per CTA
+constexpr float kTcThreshold = 8.f;
+// TMEM columns: S_0 [0,128), S_1 [128,256), O_0 [256,..), O_1 [384,..)
+constexpr uint32_t kTcO = 256;
 
-// The sequence that row t belongs to (-1: none), found by the whole warp.
-__device__ __forceinline__ int find_seq(const int32_t* cu, int nseq, int T, int t, int& lo, int& hi) {
-  const int lane = threadIdx.x & 31;
-  for (int s0 = 0; s0 < nseq; s0 += 32) {
-    const int s = s0 + lane;
-    int l = 0, h = 0;
-    if (s < nseq) seq_rows(cu, s, T, l, h);
-    const unsigned hit = __ballot_sync(0xffffffffu, t >= l && t < h);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      lo = __shfl_sync(0xffffffffu, l, src);
-      hi = __shfl_sync(0xffffffffu, h, src);
-      return s0 + src;
-    }
-  }
-  return -1;
+template <int D>
+struct TcSmem {
+  static constexpr int kTileBytes = D * 256;  // 128 rows of D 16-bit values
+  static constexpr int kQ = 0;
+  static constexpr int kK = kQ + 2 * kTileBytes;
+  static constexpr int kV = kK + 2 * kTileBytes;
+  static constexpr int kXch = kV + 2 * kTileBytes;  // chain 1's row maxima and sums
+  static constexpr int kBars = kXch + 2 * 128 * 4;
+  static constexpr int kMisc = kBars + 24 * 8;
+  static constexpr int kBytes = kMisc + 64;
+  static constexpr size_t bytes() { return 1024 + kBytes; }
+};
+static_assert(TcSmem<128>::bytes() <= 232448, "shared memory budget");
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
 }
 
-template <typename T, int D>
-__device__ __forceinline__ float row_dot(const float (&q)[D / 32], const T* k) {
-  const int lane = threadIdx.x & 31;
-  float s = 0.f;
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e) s = fmaf(q[e], to_f32(k[lane + 32 * e]), s);
-  return warp_sum(s);
+// Two floats in one 64-bit register: packed fp32 arithmetic of sm_100.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kRowThreads) prompt_rows_kernel(PromptArgs a) {
-  const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
-  if (row >= (long long)a.Tq * a.Hq) return;
-  const int t = (int)(row / a.Hq), h = (int)(row % a.Hq), hk = h / a.G;
-  int q0, q1, k0, k1;
-  const int s = find_seq(a.cu_q, a.nseq, a.Tq, t, q0, q1);
-  if (s < 0) return;
-  seq_rows(a.cu_k, s, a.Tk, k0, k1);
-  const int nk = k1 - k0;
-  const int seen = a.causal ? min(nk, t - q0 + 1 + nk - (q1 - q0)) : nk;
-  const T* q = static_cast<const T*>(a.Q) + t * a.q_tok + h * a.q_head;
-  const T* k = static_cast<const T*>(a.K) + k0 * a.k_tok + hk * a.k_head;
-  const T* v = static_cast<const T*>(a.V) + k0 * a.v_tok + hk * a.v_head;
-  float qf[D / 32], o[D / 32];
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e) {
-    qf[e] = to_f32(q[lane + 32 * e]);
-    o[e] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  for (int j = 0; j < seen; ++j) {
-    const float x = row_dot<T, D>(qf, k + j * a.k_tok) * a.scale_log2;
-    const float mn = fmaxf(m, x);
-    const float base = mn == -INFINITY ? 0.f : mn;
-    const float alpha = exp2f(m - base), p = exp2f(x - base);
-    l = l * alpha + p;
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) o[e] = o[e] * alpha + p * to_f32(v[j * a.v_tok + lane + 32 * e]);
-    m = mn;
-  }
-  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-  T* dst = static_cast<T*>(a.O) + t * a.o_tok + h * a.o_head;
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e) dst[lane + 32 * e] = from_f32<T>(o[e] * inv);
-  if (a.lse && lane == 0) a.lse[(size_t)h * a.Tq + t] = (m + log2f(l)) * kLn2;
+// Coefficients of the polynomial below (minimax by Remez exchange, rounded to fp32).
+constexpr float kEx2c0 = 0.9999992847442627f, kEx2c1 = 0.6931217908859253f, kEx2c2 = 0.240247443318367f,
+                kEx2c3 = 0.05591785907745361f, kEx2c4 = 0.009570102207362652f;
+
+// 2^x of two values on the FMA pipe: x = n + f with n the nearest integer
+// (adding 1.5 * 2^23 leaves n in the low mantissa bits) and 2^f, |f| <= 1/2, by
+// the degree-4 polynomial with the smallest relative error (2.6e-6); n is added to the exponent.  x below -126 gives 2^-126.
+__device__ __forceinline__ uint64_t ex2_poly2(uint64_t x2) {
+  float a, b;
+  unpack2(x2, a, b);
+  asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(a));  // -126
+  asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(b));
+  const uint64_t x = pack2(a, b);
+  const uint64_t big = pack2(12582912.f, 12582912.f), nbig = pack2(-12582912.f, -12582912.f);
+  const uint64_t n = add2(x, big);
+  const uint64_t f = fma2(add2(n, nbig), pack2(-1.f, -1.f), x);
+  uint64_t p = pack2(kEx2c4, kEx2c4);
+  p = fma2(p, f, pack2(kEx2c3, kEx2c3));
+  p = fma2(p, f, pack2(kEx2c2, kEx2c2));
+  p = fma2(p, f, pack2(kEx2c1, kEx2c1));
+  p = fma2(p, f, pack2(kEx2c0, kEx2c0));
+  float n0, n1, p0, p1;
+  unpack2(n, n0, n1);
+  unpack2(p, p0, p1);
+  return pack2(__uint_as_float(__float_as_uint(p0) + (__float_as_uint(n0) << 23)),
+               __uint_as_float(__float_as_uint(p1) + (__float_as_uint(n1) << 23)));
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kRowThreads) key_weights_rows_kernel(PromptArgs a) {
-  const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
-  if (row >= (long long)a.Tk * a.Hkv) return;
-  const int j = (int)(row / a.Hkv), hk = (int)(row % a.Hkv);
-  int q0, q1, k0, k1;
-  const int s = find_seq(a.cu_k, a.nseq, a.Tk, j, k0, k1);
-  if (s < 0) return;
-  seq_rows(a.cu_q, s, a.Tq, q0, q1);
-  const int first = a.causal ? max(0, (j - k0) - ((k1 - k0) - (q1 - q0))) : 0;
-  const T* k = static_cast<const T*>(a.K) + j * a.k_tok + hk * a.k_head;
-  float kf[D / 32], w = 0.f;
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e) kf[e] = to_f32(k[lane + 32 * e]);
-  for (int g = 0; g < a.G; ++g) {
-    const int h = hk * a.G + g;
-    for (int t = q0 + first; t < q1; ++t) {
-      const float lse = a.lse[(size_t)h * a.Tq + t];
-      const float x = row_dot<T, D>(kf, static_cast<const T*>(a.Q) + t * a.q_tok + h * a.q_head) * a.scale_log2;
-      w += lse == -INFINITY ? 0.f : exp2f(x - lse * kLog2E);
-    }
-  }
-  if (lane == 0) a.weights[(size_t)hk * a.Tk + j] += w;
+template <typename T>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if constexpr (std::is_same<T, __half>::value) return pack_f16x2(lo, hi);
+  return pack_bf16x2(lo, hi);
 }
 }  // namespace
 
-size_t prompt_attention_ws(const PromptArgs&) { return 256; }
-size_t key_weights_ws(const PromptArgs&) { return 256; }
+struct TcArgs {
+  const void* Q;
+  void* O;
+  float* lse;       // [Hq, Tq] natural log, or null
+  float* o_part;    // [nsplit, Tq, Hq, D] (nsplit > 1 or partial)
+  float* lse_part;  // [nsplit, Tq, Hq] log2
+  const int32_t* cu_q;  // null: one sequence of Tq and Tk rows
+  const int32_t* cu_k;
+  int nseq, Hq, Hkv, G, Tq, Tk, causal, nsplit, ntile;
+  bool partial;  // write o_part / lse_part
+  float scale_log2;
+  int64_t q_tok, q_head, o_tok, o_head;
+};
 
-template <typename F>
-static cudaError_t by_type(int dtype, int d, F f) {
-  if (dtype == IG_BF16) return d == 128 ? f((__nv_bfloat16)0.f, std::integral_constant<int, 128>())
-                                        : f((__nv_bfloat16)0.f, std::integral_constant<int, 64>());
-  return d == 128 ? f((__half)0.f, std::integral_constant<int, 128>())
-                  : f((__half)0.f, std::integral_constant<int, 64>());
+// Row tile pair -> sequence.  Sequence s owns the pair numbers [f(s), f(s+1)),
+// f(s) = floor(cu_q[s] G / 256) + s: at least ceil(n_q G / 256) of them (the
+// others are idle), and f needs no sum over the sequences before, so a warp
+// finds s by a 32-way search.
+__device__ __forceinline__ int first_pair(const int32_t* cu, int s, int G) {
+  return (int)(((long long)cu[s] * G) >> 8) + s;
+}
+__device__ __forceinline__ int find_pair(const int32_t* cu, int nseq, int G, int t, int& local) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = nseq;
+  bool found = false;
+  while (hi - lo > 1 || !found) {
+    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+    const unsigned hit = __ballot_sync(0xffffffffu, at < hi && first_pair(cu, at, G) <= t);
+    if (!hit) return -1;
+    lo += (31 - __clz(hit)) * step;
+    hi = min(hi, lo + step);
+    found = true;
+  }
+  local = t - first_pair(cu, lo, G);
+  return lo;
 }
 
-cudaError_t launch_prompt_attention(const PromptArgs& a, cudaStream_t s) {
-  const long long rows = (long long)a.Tq * a.Hq;
-  if (rows == 0) return cudaSuccess;
-  return by_type(a.dtype, a.d, [&](auto t, auto d) {
-    prompt_rows_kernel<decltype(t), decltype(d)::value>
-        <<<(unsigned)((rows + 3) / 4), kRowThreads, 0, s>>>(a);
-    return cudaGetLastError();
-  });
+template <typename T, int D>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    attend_kernel(TcArgs a, const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v) {
+  using L = TcSmem<D>;
+  constexpr bool kHalf = std::is_same<T, __half>::value;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* xch = reinterpret_cast<float*>(smem + L::kXch);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
+  uint64_t* q_full = bars + 0;   // [2] row tiles
+  uint64_t* k_full = bars + 2;   // [2] stages
+  uint64_t* k_empty = bars + 4;  // [2]
+  uint64_t* v_full = bars + 6;   // [2]
+  uint64_t* v_empty = bars + 8;  // [2]
+  uint64_t* s_full = bars + 10;  // [2] chains
+  uint64_t* p_head = bars + 12;  // [2] chains: the tile's first 96 keys of P
+  uint64_t* p_tail = bars + 14;  // [2] chains: the last 32
+  uint64_t* o_done = bars + 16;  // [2] chains
+  uint64_t* fin = bars + 18;     // [2] chains
+  uint64_t* v_fixed = bars + 20;
+  int* misc = reinterpret_cast<int*>(smem + L::kMisc);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(misc + 0);
+  volatile int* abort_flag = misc + 1;
+  int* work = misc + 2;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int hk = blockIdx.x % a.Hkv;
+  const int t_glob = (blockIdx.x / a.Hkv) % a.ntile;
+  const int z = blockIdx.x / a.Hkv / a.ntile;
+
+  // ---- which rows
+  int q0s = 0, q1s = a.Tq, k0s = 0, k1s = a.Tk, local = t_glob;
+  if (a.cu_q) {
+    if (warp == 0) {
+      int lp = 0;
+      const int s = find_pair(a.cu_q, a.nseq, a.G, t_glob, lp);
+      if (lane == 0) {
+        work[0] = s;
+        work[1] = lp;
+      }
+    }
+    __syncthreads();
+    const int s = work[0];
+    if (s < 0) return;
+    local = work[1];
+    seq_rows(a.cu_q, s, a.Tq, q0s, q1s);
+    seq_rows(a.cu_k, s, a.Tk, k0s, k1s);
+  }
+  const int nq = q1s - q0s, nk = k1s - k0s, G = a.G;
+  const int R = nq * G;
+  // the last rows of a sequence see the most keys: they go first
+  const int pair = (R + kTcRows - 1) / kTcRows - 1 - local;
+  if (pair < 0 || local < 0) return;
+  const int r0 = pair * kTcRows;
+  const int rows0 = min(128, R - r0), rows1 = max(0, min(128, R - r0 - 128));
+  const bool one = rows1 == 0;  // one row tile: chains take the even / odd key tiles
+  auto seen = [&](int r) { return a.causal ? min(nk, max(0, r / G + 1 + nk - nq)) : nk; };  // keys that row r sees
+  // key tiles [j0, j1) of this CTA; chain t's end
+  const int ntk = (seen(r0 + rows0 + rows1 - 1) + 127) / 128;
+  const int j0 = (int)((long long)ntk * z / a.nsplit), j1 = (int)((long long)ntk * (z + 1) / a.nsplit);
+  const int end0 = one ? j1 : max(j0, min(j1, (seen(r0 + rows0 - 1) + 127) / 128));
+  const int nj = j1 - j0;
+  const int cut = nk & 127 ? nk >> 7 : -1;  // the key tile that the sequence ends in
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 128);
+      mbar_init(&k_full[i], 1);
+      mbar_init(&v_full[i], 1);
+      mbar_init(&k_empty[i], one ? 1 : 2);
+      mbar_init(&v_empty[i], one ? 1 : 2);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_head[i], 128);
+      mbar_init(&p_tail[i], 128);
+      mbar_init(&o_done[i], 1);
+      mbar_init(&fin[i], 1);
+    }
+    mbar_init(v_fixed, 32);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const uint32_t q_s = smem_u32(smem + L::kQ);
+  const uint32_t k_s = smem_u32(smem + L::kK);
+  const uint32_t v_s = smem_u32(smem + L::kV);
+  constexpr int kChunks = D / 8;             // 16-byte chunks of a row
+  constexpr int kRowsPerStep = 32 / kChunks; // rows a warp moves at once
+
+  if (warp >= 8) {
+    setmaxnreg_dec<72>();
+    if (warp == 10) {
+      // ============================================================= loader
+      for (int i = 0; i < nj; ++i) {
+        const int s = i & 1, row = k0s + (j0 + i) * 128;
+        if (i >= 2 && !mbar_wait_warp(&k_empty[s], ((i >> 1) - 1) & 1, abort_flag)) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&k_full[s], L::kTileBytes);
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(k_s + s * L::kTileBytes + c * 16384, &tmap_k, 64 * c, row, hk, &k_full[s]);
+        }
+        if (i >= 2 && !mbar_wait_warp(&v_empty[s], ((i >> 1) - 1) & 1, abort_flag)) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&v_full[s], L::kTileBytes);
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(v_s + s * L::kTileBytes + c * 16384, &tmap_v, 64 * c, row, hk, &v_full[s]);
+        }
+        if (j0 + i == cut) {  // zero the V rows behind the sequence's end
+          if (!mbar_wait_warp(&v_full[s], (i >> 1) & 1, abort_flag)) break;
+          for (int c = 0; c < D / 64; ++c)
+            for (int b = (nk & 127) * 8 + lane; b < 1024; b += 32)
+              st_shared_v4(v_s + s * L::kTileBytes + c * 16384 + b * 16, 0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+          mbar_arrive(v_fixed);
+        }
+      }
+    } else if (warp < 10) {
+      // ================================================================ MMA
+      // warp 8 + t issues chain t: S_t(first), then PV_t(previous), S_t(next),
+      // ... PV_t(last); the warp waits in step, one elected lane issues
+      const int t = warp - 8;
+      const uint32_t idesc_qk = umma_idesc_f16kind(128, 128, false, false, kHalf);
+      const uint32_t idesc_pv = umma_idesc_f16kind(128, D, false, true, kHalf);
+      constexpr uint64_t kTileStep = (uint64_t)(L::kTileBytes >> 4);
+      const uint64_t qd = umma_desc_sw128(q_s, 16, 1024) + (uint64_t)(one ? 0 : t) * kTileStep;
+      const uint64_t kd0 = umma_desc_sw128(k_s, 16, 1024);
+      const uint64_t vd0 = umma_desc_sw128(v_s, 16384, 1024);
+      const uint32_t s_t = tmem + 128 * t, o_t = tmem + kTcO + 128 * t;
+      const int step = one ? 2 : 1, i0 = one ? t : 0;
+      const int iend = (!one && t == 0 ? end0 : j1) - j0;
+      bool ok = true;
+      auto issue_pv = [&](int i, int ph) -> bool {
+        if (!mbar_wait_warp(&v_full[i & 1], (i >> 1) & 1, abort_flag)) return false;
+        if (j0 + i == cut && !mbar_wait_warp(v_fixed, 0, abort_flag)) return false;
+        if (!mbar_wait_warp(&p_head[t], ph & 1, abort_flag)) return false;
+        tc_fence_after();
+        const uint64_t vd = vd0 + (uint64_t)(i & 1) * kTileStep;
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 6; ++k)
+            umma_f16_ts(o_t, s_t + 8 * k, vd + (uint64_t)(k * 128), idesc_pv, (ph > 0 || k > 0) ? 1u : 0u);
+        }
+        __syncwarp();
+        if (!mbar_wait_warp(&p_tail[t], ph & 1, abort_flag)) return false;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 6; k < 8; ++k) umma_f16_ts(o_t, s_t + 8 * k, vd + (uint64_t)(k * 128), idesc_pv, 1u);
+          umma_commit(&v_empty[i & 1]);
+        }
+        __syncwarp();
+        return true;
+      };
+      auto issue_s = [&](int i) -> bool {
+        if (!mbar_wait_warp(&k_full[i & 1], (i >> 1) & 1, abort_flag)) return false;
+        tc_fence_after();
+        const uint64_t kd = kd0 + (uint64_t)(i & 1) * kTileStep;
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t off = (uint64_t)((k >> 2) * 1024 + (k & 3) * 2);
+            umma_bf16_ss(s_t, qd + off, kd + off, idesc_qk, k > 0 ? 1u : 0u);
+          }
+          umma_commit(&s_full[t]);
+          umma_commit(&k_empty[i & 1]);
+        }
+        __syncwarp();
+        return true;
+      };
+      if (i0 < iend) {
+        ok = mbar_wait_warp(&q_full[one ? 0 : t], 0, abort_flag);
+        fence_proxy_async_smem();
+        int prev = -1, ph = 0;
+        for (int i = i0; i < iend && ok; i += step) {
+          if (prev >= 0) {
+            ok = issue_pv(prev, ph++);
+            if (!ok) break;
+          }
+          ok = issue_s(i);
+          prev = i;
+        }
+        if (ok) ok = issue_pv(prev, ph);
+      }
+      if (elect_one()) {
+        if (ok) umma_commit(&o_done[t]);
+        umma_commit(&fin[t]);
+      }
+      __syncwarp();
+      // key tiles that only chain 1 reads: hand the stages on for it
+      if (!one && t == 0) {
+        for (int i = max(0, iend); i < nj && ok; ++i) {
+          ok = mbar_wait_warp(&k_full[i & 1], (i >> 1) & 1, abort_flag) &&
+               mbar_wait_warp(&v_full[i & 1], (i >> 1) & 1, abort_flag);
+          if (ok && lane == 0) {
+            mbar_arrive(&k_empty[i & 1]);
+            mbar_arrive(&v_empty[i & 1]);
+          }
+        }
+      }
+      mbar_wait_drain(&fin[t], 0);
+    }
+  } else {
+    // ============================================================== softmax
+    setmaxnreg_inc<216>();
+    const int t = warp >> 2, qd = warp & 3;
+    const int r = 32 * qd + lane;  // row of the tile == TMEM lane
+    const int nrows = t == 0 ? rows0 : rows1;
+    const int rt = r0 + 128 * t;   // first row of the tile
+    const uint32_t lane_off = (uint32_t)((32 * qd) << 16);
+    const uint32_t s_col = tmem + lane_off + 128 * t, o_col = tmem + lane_off + kTcO + 128 * t;
+    // this warp's 32 query rows, whole rows at a time
+    {
+      const int rr = rt + r;
+      const int64_t off = r < nrows ? (q0s + rr / G) * a.q_tok + (hk * G + rr % G) * a.q_head : -1;
+      const T* Q = static_cast<const T*>(a.Q);
+      const int ch = lane % kChunks;
+      if (nrows > 0) {
+#pragma unroll
+        for (int i = 0; i < 32 / kRowsPerStep; ++i) {
+          const int from = i * kRowsPerStep + lane / kChunks;
+          const int64_t o = __shfl_sync(0xffffffffu, off, from);
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (o >= 0) v = __ldg(reinterpret_cast<const uint4*>(Q + o) + ch);
+          st_shared_v4(q_s + t * L::kTileBytes + (ch >> 3) * 16384 + sw128_offset(32 * qd + from, ch & 7), v.x, v.y,
+                       v.z, v.w);
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&q_full[t]);
+    }
+    const int see = one || t == 0 ? (r < rows0 ? seen(r0 + r) : 0) : (r < rows1 ? seen(rt + r) : 0);
+    // tiles below `whole` need no mask in any row of the tile
+    const int whole = (one ? seen(r0) : seen(min(rt, R - 1))) >> 7;
+    float m = -INFINITY, l = 0.f;
+    const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
+    bool ok = true;
+    const int step = one ? 2 : 1;
+    const int jend = !one && t == 0 ? end0 : j1;
+    int ph = 0;
+
+    auto visit = [&](int j, auto masked) {
+      constexpr bool kMask = decltype(masked)::value;
+      float x4[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, x4[c]);
+      tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) pin_regs32(x4[c]);
+      if constexpr (kMask) {
+        const int lim = see - j * 128;
+#pragma unroll
+        for (int c = 0; c < 128; ++c) x4[c >> 5][c & 31] = c < lim ? x4[c >> 5][c & 31] : -INFINITY;
+      }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int c = 0; c < 128; c += 2)
+        mx[(c >> 1) & 3] = fmax3(mx[(c >> 1) & 3], x4[c >> 5][c & 31], x4[c >> 5][(c & 31) + 1]);
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+      const bool raise = top > m + kTcThreshold;  // the first key of a row always raises
+      float alpha = 1.f;
+      if (raise) {
+        alpha = ex2_approx(m - top);
+        m = top;
+      }
+      // O_t holds the chain's earlier products (the tensor pipe finished them
+      // before S_t(j)); the next one waits for p_head
+      if (ph > 0 && __any_sync(0xffffffffu, raise)) {
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          float o[32];
+          tmem_ld32(o_col + 32 * c, o);
+          tmem_wait_ld();
+          pin_regs32(o);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] *= alpha;
+          tmem_st32(o_col + 32 * c, o);
+        }
+      }
+      const float base = m == -INFINITY ? 0.f : -m;  // no key so far: 2^(-inf) = 0
+      const uint64_t base2 = pack2(base, base);
+      uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+      for (int c4 = 0; c4 < 4; ++c4) {
+        uint32_t p[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          uint64_t y = fma2(pack2(x4[c4][e], x4[c4][e + 1]), scale2, base2);
+          float p0, p1;
+          if (!kMask && (e & 6) == 6) {
+            y = ex2_poly2(y);
+            unpack2(y, p0, p1);
+          } else {
+            unpack2(y, p0, p1);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+            y = pack2(p0, p1);
+          }
+          sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], y);
+          p[e >> 1] = pack16<T>(p0, p1);
+        }
+        tmem_st16(s_col + 16 * c4, p);
+        if (c4 == 2) {
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&p_head[t]);
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&p_tail[t]);
+      float s0, s1;
+      unpack2(add2(sum[0], sum[1]), s0, s1);
+      l = l * alpha + (s0 + s1);
+    };
+
+    for (int j = j0 + (one ? t : 0); j < jend; j += step, ++ph) {
+      if (!mbar_wait_warp(&s_full[t], ph & 1, abort_flag)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      if (j < whole)
+        visit(j, std::false_type());
+      else
+        visit(j, std::true_type());
+    }
+    if (ok) ok = mbar_wait_warp(&o_done[t], 0, abort_flag);
+    tc_fence_after();
+    bool have = ph > 0;  // O_t was written
+    float w0 = 1.f, w1 = 0.f;
+    bool have1 = false;
+    if (one) {
+      // merge the two chains' partial softmaxes of the same rows
+      if (t == 1) {
+        xch[r] = m;
+        xch[128 + r] = l;
+      }
+      named_bar_sync(1, 256);
+      if (t == 0) {
+        have1 = nj > 1;
+        if (ok) ok = mbar_wait_warp(&o_done[1], 0, abort_flag);
+        tc_fence_after();
+        const float m1 = xch[r], l1 = xch[128 + r];
+        const float mm = fmaxf(m, m1);
+        w0 = m == -INFINITY ? 0.f : ex2_approx(m - mm);
+        w1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - mm);
+        l = l * w0 + l1 * w1;
+        m = mm;
+      }
+    }
+    if (ok && nrows > 0) {
+      const int rr = rt + r;
+      const int tok = q0s + rr / G, head = hk * G + rr % G;
+      const bool valid = r < nrows;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      if (valid) {
+        const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
+        if (a.partial)
+          a.lse_part[((size_t)z * a.Tq + tok) * a.Hq + head] = lse2;
+        else if (a.lse)
+          a.lse[(size_t)head * a.Tq + tok] = lse2 * kLn2;
+      }
+      if (!a.partial || have) {
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          float o[32];
+          if (have) {
+            tmem_ld32(o_col + 32 * c, o);
+            tmem_wait_ld();
+            pin_regs32(o);
+            if (have1) {
+              float o1[32];
+              tmem_ld32(o_col + 128 + 32 * c, o1);
+              tmem_wait_ld();
+              pin_regs32(o1);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = o[e] * w0 + o1[e] * w1;
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = have && l != 0.f ? o[e] * inv : 0.f;
+          if (a.partial) {
+            if (valid) {
+              float4* dst =
+                  reinterpret_cast<float4*>(a.o_part + (((size_t)z * a.Tq + tok) * a.Hq + head) * D + 32 * c);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            }
+          } else {
+            // staged in the row tile's shared memory (no MMA reads Q any more)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              st_shared_v4(q_s + t * L::kTileBytes + (c >> 1) * 16384 + sw128_offset(r, (4 * c + e) & 7),
+                           pack16<T>(o[8 * e], o[8 * e + 1]), pack16<T>(o[8 * e + 2], o[8 * e + 3]),
+                           pack16<T>(o[8 * e + 4], o[8 * e + 5]), pack16<T>(o[8 * e + 6], o[8 * e + 7]));
+          }
+        }
+        if (!a.partial) {
+          __syncwarp();
+          const int64_t off = valid ? tok * a.o_tok + head * a.o_head : -1;
+          T* O = static_cast<T*>(a.O);
+          const int ch = lane % kChunks;
+#pragma unroll
+          for (int i = 0; i < 32 / kRowsPerStep; ++i) {
+            const int from = i * kRowsPerStep + lane / kChunks;
+            const int64_t o = __shfl_sync(0xffffffffu, off, from);
+            const uint4 v = *reinterpret_cast<const uint4*>(smem + L::kQ + t * L::kTileBytes + (ch >> 3) * 16384 +
+                                                            sw128_offset(32 * qd + from, ch & 7));
+            if (o >= 0) reinterpret_cast<uint4*>(O + o)[ch] = v;
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
 }
 
-cudaError_t launch_key_weights(const PromptArgs& a, cudaStream_t s) {
-  const long long rows = (long long)a.Tk * a.Hkv;
-  if (rows == 0 || a.Tq == 0) return cudaSuccess;
-  return by_type(a.dtype, a.d, [&](auto t, auto d) {
-    key_weights_rows_kernel<decltype(t), decltype(d)::value>
-        <<<(unsigned)((rows + 3) / 4), kRowThreads, 0, s>>>(a);
-    return cudaGetLastError();
-  });
+// Joins the partial outputs of rows (token, head) over the splits: weights
+// 2^(lse_z - max) / sum.  One warp per row.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) combine_kernel(TcArgs a) {
+  const int lane = threadIdx.x & 31;
+  const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const size_t rows = (size_t)a.Tq * a.Hq;
+  if (row >= (long long)rows) return;
+  const int tok = (int)(row / a.Hq), head = (int)(row % a.Hq);
+  if (a.cu_q) {  // rows of no sequence stay as they were
+    int lo = 0, hi = a.nseq;
+    bool found = false;
+    while (hi - lo > 1 || !found) {
+      const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+      const unsigned hit = __ballot_sync(0xffffffffu, at < hi && a.cu_q[at] <= tok);
+      if (!hit) return;
+      lo += (31 - __clz(hit)) * step;
+      hi = min(hi, lo + step);
+      found = true;
+    }
+    if (tok >= a.cu_q[lo + 1]) return;
+  }
+  float top = -INFINITY;
+  for (int z = 0; z < a.nsplit; ++z) top = fmaxf(top, a.lse_part[z * rows + row]);
+  float o[D / 32], sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
+  for (int z = 0; z < a.nsplit; ++z) {
+    const float x = a.lse_part[z * rows + row];
+    if (x == -INFINITY) continue;
+    const float w = exp2f(x - top);
+    sum += w;
+    const float* src = a.o_part + (z * rows + row) * D;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) o[e] = fmaf(w, src[lane + 32 * e], o[e]);
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  T* dst = static_cast<T*>(a.O) + tok * a.o_tok + head * a.o_head;
+#pragma unroll
+  for (int e = 0; e < D / 32; ++e) dst[lane + 32 * e] = from_f32<T>(o[e] * inv);
+  if (a.lse && lane == 0) a.lse[(size_t)head * a.Tq + tok] = (top + log2f(sum)) * kLn2;
+}
+
+// ------------------------------------------------------------------- host
+// [heads, rows, d] 16-bit tensor with strides (elements), boxes of 128 rows x
+// 64 columns in the UMMA 128-byte swizzle.
+static cudaError_t make_tmap_rows(CUtensorMap* m, const void* base, int dtype, int d, int rows, int heads, int64_t tok,
+                                  int64_t head) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return cudaErrorUnknown;
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)heads};
+  cuuint64_t strides[2] = {(cuuint64_t)tok * 2, (cuuint64_t)head * 2};
+  cuuint32_t box[3] = {64, 128, 1}, estr[3] = {1, 1, 1};
+  const CUresult r = fn(m, dtype == IG_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                        const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+constexpr int kSms = 148;
+
+// Row tile pairs of packed sequences (an upper bound, see find_pair).
+static long long row_pairs(int Tq, int G, int nseq) { return ((long long)Tq * G >> 8) + nseq; }
+
+// CTAs per row tile pair: where the pairs leave SMs idle, the keys are split
+// so that about every SM has a CTA, in parts of at least 4 key tiles.
+static int key_splits(long long ctas, long long keys) {
+  if (ctas >= kSms) return 1;
+  const long long by_keys = keys / 512;
+  long long n = kSms / ctas;
+  if (n > by_keys) n = by_keys;
+  if (n > 64) n = 64;
+  return n < 1 ? 1 : (int)n;
+}
+
+template <typename T, int D>
+static cudaError_t run_attend(const TcArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+  const size_t sm = TcSmem<D>::bytes();
+  cudaError_t e = cudaFuncSetAttribute(attend_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+  if (e != cudaSuccess) return e;
+  attend_kernel<T, D><<<(unsigned)((long long)a.ntile * a.Hkv * a.nsplit), kTcThreads, sm, s>>>(a, tk, tv);
+  return cudaGetLastError();
+}
+
+static cudaError_t dispatch_attend(const TcArgs& a, int dtype, int d, const CUtensorMap& tk, const CUtensorMap& tv,
+                                   cudaStream_t s) {
+  if (dtype == IG_BF16)
+    return d == 128 ? run_attend<__nv_bfloat16, 128>(a, tk, tv, s) : run_attend<__nv_bfloat16, 64>(a, tk, tv, s);
+  return d == 128 ? run_attend<__half, 128>(a, tk, tv, s) : run_attend<__half, 64>(a, tk, tv, s);
+}
+
+static int prompt_splits(const PromptArgs& a) {
+  return key_splits(row_pairs(a.Tq, a.G, a.nseq) * a.Hkv, a.Tk / a.nseq);
+}
+
+size_t prompt_attention_ws(const PromptArgs& a) {
+  const int n = prompt_splits(a);
+  return n == 1 ? 256 : (size_t)n * a.Tq * a.Hq * (a.d + 1) * 4;
+}
+
+cudaError_t launch_prompt_attention(const PromptArgs& p, cudaStream_t s) {
+  TcArgs a{};
+  a.Q = p.Q;
+  a.O = p.O;
+  a.lse = p.lse;
+  a.cu_q = p.cu_q;
+  a.cu_k = p.cu_k;
+  a.nseq = p.nseq;
+  a.Hq = p.Hq;
+  a.Hkv = p.Hkv;
+  a.G = p.G;
+  a.Tq = p.Tq;
+  a.Tk = p.Tk;
+  a.causal = p.causal;
+  a.scale_log2 = p.scale_log2;
+  a.q_tok = p.q_tok;
+  a.q_head = p.q_head;
+  a.o_tok = p.o_tok;
+  a.o_head = p.o_head;
+  a.ntile = (int)row_pairs(p.Tq, p.G, p.nseq);
+  a.nsplit = prompt_splits(p);
+  a.partial = a.nsplit > 1;
+  a.o_part = static_cast<float*>(p.ws);
+  a.lse_part = a.o_part + (size_t)a.nsplit * p.Tq * p.Hq * p.d;
+  CUtensorMap tk, tv;
+  // without any key rows no load is issued; the maps then only need an address
+  cudaError_t e = make_tmap_rows(&tk, p.Tk ? p.K : p.Q, p.dtype, p.d, p.Tk ? p.Tk : 1, p.Hkv, p.k_tok, p.k_head);
+  if (e == cudaSuccess)
+    e = make_tmap_rows(&tv, p.Tk ? p.V : p.Q, p.dtype, p.d, p.Tk ? p.Tk : 1, p.Hkv, p.v_tok, p.v_head);
+  if (e == cudaSuccess) e = dispatch_attend(a, p.dtype, p.d, tk, tv, s);
+  if (e != cudaSuccess || !a.partial) return e;
+  const unsigned grid = (unsigned)(((long long)p.Tq * p.Hq + 3) / 4);
+  if (p.dtype == IG_BF16) {
+    if (p.d == 128)
+      combine_kernel<__nv_bfloat16, 128><<<grid, 128, 0, s>>>(a);
+    else
+      combine_kernel<__nv_bfloat16, 64><<<grid, 128, 0, s>>>(a);
+  } else {
+    if (p.d == 128)
+      combine_kernel<__half, 128><<<grid, 128, 0, s>>>(a);
+    else
+      combine_kernel<__half, 64><<<grid, 128, 0, s>>>(a);
+  }
+  return cudaGetLastError();
 }
 
 }  // namespace ig
