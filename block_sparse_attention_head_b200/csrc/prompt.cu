@@ -83,27 +83,33 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// Coefficients of the polynomial below (minimax by Remez exchange, rounded to fp32).
-constexpr float kEx2c0 = 0.9999992847442627f, kEx2c1 = 0.6931217908859253f, kEx2c2 = 0.240247443318367f,
-                kEx2c3 = 0.05591785907745361f, kEx2c4 = 0.009570102207362652f;
-
 // 2^x of two values on the FMA pipe: x = n + f with n the nearest integer
 // (adding 1.5 * 2^23 leaves n in the low mantissa bits) and 2^f, |f| <= 1/2, by
-// the degree-4 polynomial with the smallest relative error (2.6e-6); n is added to the exponent.  x below -126 gives 2^-126.
+// the degree-4 or degree-5 polynomial with the smallest relative error (2.6e-6
+// and 1.6e-7; Remez exchange, coefficients rounded to fp32); n is added to the
+// exponent.  x below -126 gives 2^-126.
+template <int kDegree>
 __device__ __forceinline__ uint64_t ex2_poly2(uint64_t x2) {
+  constexpr float c0 = kDegree == 5 ? 1.0000001192092896f : 0.9999992847442627f;
+  constexpr float c1 = kDegree == 5 ? 0.6931469440460205f : 0.6931217908859253f;
+  constexpr float c2 = kDegree == 5 ? 0.24022120237350464f : 0.240247443318367f;
+  constexpr float c3 = kDegree == 5 ? 0.05550713092088699f : 0.05591785907745361f;
+  constexpr float c4 = kDegree == 5 ? 0.009675540961325169f : 0.009570102207362652f;
+  constexpr float c5 = 0.0013276472454890609f;
+  static_assert(kDegree == 4 || kDegree == 5, "degree");
   float a, b;
   unpack2(x2, a, b);
   asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(a));  // -126
   asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(b));
   const uint64_t x = pack2(a, b);
-  const uint64_t big = pack2(12582912.f, 12582912.f), nbig = pack2(-12582912.f, -12582912.f);
-  const uint64_t n = add2(x, big);
-  const uint64_t f = fma2(add2(n, nbig), pack2(-1.f, -1.f), x);
-  uint64_t p = pack2(kEx2c4, kEx2c4);
-  p = fma2(p, f, pack2(kEx2c3, kEx2c3));
-  p = fma2(p, f, pack2(kEx2c2, kEx2c2));
-  p = fma2(p, f, pack2(kEx2c1, kEx2c1));
-  p = fma2(p, f, pack2(kEx2c0, kEx2c0));
+  const uint64_t n = add2(x, pack2(12582912.f, 12582912.f));
+  const uint64_t f = fma2(add2(n, pack2(-12582912.f, -12582912.f)), pack2(-1.f, -1.f), x);
+  uint64_t p = pack2(c4, c4);
+  if constexpr (kDegree == 5) p = fma2(pack2(c5, c5), f, p);
+  p = fma2(p, f, pack2(c3, c3));
+  p = fma2(p, f, pack2(c2, c2));
+  p = fma2(p, f, pack2(c1, c1));
+  p = fma2(p, f, pack2(c0, c0));
   float n0, n1, p0, p1;
   unpack2(n, n0, n1);
   unpack2(p, p0, p1);
@@ -254,6 +260,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     setmaxnreg_dec<72>();
     if (warp == 10) {
       // ============================================================= loader
+      int issued = 0;
       for (int i = 0; i < nj; ++i) {
         const int s = i & 1, row = k0s + (j0 + i) * 128;
         if (i >= 2 && !mbar_wait_warp(&k_empty[s], ((i >> 1) - 1) & 1, abort_flag)) break;
@@ -276,6 +283,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           fence_proxy_async_smem();
           mbar_arrive(v_fixed);
         }
+        issued = i + 1;
+      }
+      for (int i = max(0, issued - 2); i < issued; ++i) {  // no copy in flight is left behind
+        mbar_wait_drain(&k_full[i & 1], (i >> 1) & 1);
+        mbar_wait_drain(&v_full[i & 1], (i >> 1) & 1);
       }
     } else if (warp < 10) {
       // ================================================================ MMA
@@ -450,7 +462,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           uint64_t y = fma2(pack2(x4[c4][e], x4[c4][e + 1]), scale2, base2);
           float p0, p1;
           if (!kMask && (e & 6) == 6) {
-            y = ex2_poly2(y);
+            y = ex2_poly2<4>(y);
             unpack2(y, p0, p1);
           } else {
             unpack2(y, p0, p1);
@@ -628,15 +640,15 @@ __global__ void __launch_bounds__(128) combine_kernel(TcArgs a) {
 }
 
 // ------------------------------------------------------------------- host
-// [heads, rows, d] 16-bit tensor with strides (elements), boxes of 128 rows x
-// 64 columns in the UMMA 128-byte swizzle.
+// [heads, rows, d] 16-bit tensor with strides (elements), boxes of box_rows
+// rows x 64 columns in the UMMA 128-byte swizzle.
 static cudaError_t make_tmap_rows(CUtensorMap* m, const void* base, int dtype, int d, int rows, int heads, int64_t tok,
-                                  int64_t head) {
+                                  int64_t head, unsigned box_rows = 128) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return cudaErrorUnknown;
   cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)heads};
   cuuint64_t strides[2] = {(cuuint64_t)tok * 2, (cuuint64_t)head * 2};
-  cuuint32_t box[3] = {64, 128, 1}, estr[3] = {1, 1, 1};
+  cuuint32_t box[3] = {64, box_rows, 1}, estr[3] = {1, 1, 1};
   const CUresult r = fn(m, dtype == IG_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                         const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

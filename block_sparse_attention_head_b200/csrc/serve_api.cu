@@ -11,7 +11,7 @@ int check_heads(int Hq, int Hkv, int d, int dtype) {
   if (Hq < 1 || Hkv < 1 || Hq % Hkv) return IG_ERR_INVALID_ARG;
   if (dtype != IG_BF16 && dtype != IG_F16) return IG_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return IG_ERR_UNSUPPORTED;
-  if (Hkv > 65535 || Hq > 65535) return IG_ERR_UNSUPPORTED;  // grid.y
+  if (Hq > 65535 || Hq / Hkv > 1024) return IG_ERR_UNSUPPORTED;
   return IG_OK;
 }
 
@@ -33,7 +33,7 @@ int prompt_args(const instagen_prompt_params* p, ig::PromptArgs* a) {
   if (rc) return rc;
   if (!good_scale(p->softmax_scale)) return IG_ERR_INVALID_ARG;
   const long long most = 2147483647LL - 1024;
-  if (p->nseq > (1 << 20) || (long long)p->Tq * p->Hq > most || (long long)p->Tk * p->Hkv > most)
+  if (p->nseq > (1 << 20) || (long long)p->nseq * p->Hkv > (1 << 26) || (long long)p->Tq * p->Hq > most || (long long)p->Tk * p->Hkv > most)
     return IG_ERR_UNSUPPORTED;
   if (!good_strides(p->q_tok, p->q_head, p->Tq, p->Hq, p->d) || !good_strides(p->k_tok, p->k_head, p->Tk, p->Hkv, p->d))
     return IG_ERR_INVALID_ARG;

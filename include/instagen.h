@@ -371,8 +371,8 @@ int instagen_forward_layout_get(const instagen_params* p, instagen_forward_layou
 typedef enum { IG_BF16 = 0, IG_F16 = 1 } instagen_dtype;
 
 typedef struct {
-  int32_t nseq;              /* packed sequences, 1 .. 2^20                           */
-  int32_t Hq, Hkv, d;        /* heads (Hkv divides Hq); d in {64, 128}                */
+  int32_t nseq;              /* packed sequences, 1 .. 2^20 (nseq * Hkv <= 2^26)      */
+  int32_t Hq, Hkv, d;        /* heads (Hkv divides Hq, Hq / Hkv <= 1024); d in {64, 128} */
   int32_t Tq, Tk;            /* rows of Q and of K, V: >= every end in cu_q / cu_k    */
   int32_t dtype;             /* instagen_dtype of Q, K, V, O                          */
   int32_t causal;            /* 1: query i of a sequence sees its keys j <= i + n_k - n_q
@@ -414,7 +414,8 @@ int instagen_key_weights(const void* Q, const void* K, const float* lse, const i
                          const instagen_prompt_params* p, float* weights, void* ws, size_t ws_bytes, void* stream);
 
 typedef struct {
-  int32_t B, Hq, Hkv, d;     /* sequences, heads (Hkv divides Hq), d in {64, 128}     */
+  int32_t B, Hq, Hkv, d;     /* sequences, heads (Hkv divides Hq, Hq / Hkv <= 1024),
+                                d in {64, 128}; B * Hkv <= 65535                      */
   int32_t P;                 /* keys of the prefix that all sequences share, >= 0     */
   int32_t cap;               /* slots of each sequence's own cache, >= 0              */
   int32_t dtype;             /* instagen_dtype                                        */
