@@ -1,90 +1,502 @@
-// Attention of one new token per sequence over a shared prefix and its own
-// cache (instagen_prefix_attention).  Simple form: one warp per query row.
+// Attention of one new token per sequence over a prefix that the batch shares
+// and the sequence's own cache (instagen_prefix_attention).
+//
+// Three kernels write and join partial softmaxes: every part leaves its
+// normalised output rows and their log-sum-exp (log2), finish_kernel weighs
+// them by 2^(lse - max) and normalises once.
+//   prefix  The B * G query rows that read one key/value head form one matrix,
+//           so the prefix is read once for the batch: attend_kernel (tensor
+//           cores, see prompt.cu), its keys split over the SMs.
+//   own     rows_kernel: the G rows of a sequence against its own keys.  Bound
+//           by the cache's bytes (G / 2 multiply-adds per byte): a warp takes
+//           16 keys of every 64-key tile with m16n8k16 products, whose score
+//           registers are the next product's operand registers, so scores
+//           never leave the registers; tiles stream through a TMA ring.  A
+//           prefix with at most 16 rows (small batches) goes the same way, in
+//           the same launch.
+//   finish  join, and add the own keys' weights 2^(score - lse) from the scores
+//           that rows_kernel left (4 G bytes per key beside the 4 d it read).
 #include "serve.cuh"
 
 namespace ig {
 
 namespace {
+constexpr int kRowsThreads = 160;  // 4 warps of 16 keys, 1 loader
+constexpr int kRowsKeys = 64;      // keys per tile
+constexpr int kFinishKeys = 1024;  // keys per CTA of the weights' part
+
+template <int D>
+struct RowsSmem {
+  static constexpr int kTileBytes = kRowsKeys * D * 2;
+  static constexpr int kStages = D == 128 ? 3 : 6;  // 96 KB in flight, two CTAs per SM
+  static constexpr int kRing = 0;                   // [stage][K, V]
+  static constexpr int kMl = kRing + kStages * 2 * kTileBytes;  // [4 warps][16 rows] maxima, then sums
+  static constexpr int kBars = kMl + 2 * 4 * 16 * 4;
+  static constexpr int kMisc = kBars + 2 * kStages * 8;
+  static constexpr size_t bytes() { return 1024 + kMisc + 16; }
+  static_assert(4 * 16 * D * 4 <= kStages * 2 * kTileBytes, "the warps' outputs are joined in the ring");
+};
+
+__device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (std::is_same<T, __half>::value)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+}  // namespace
+
+struct RowsArgs {
+  const void* Q;
+  const int32_t* lens;
+  int B, Hq, Hkv, G, P, cap;
+  int nown;     // splits of a cache
+  int npre;     // splits of the prefix in this kernel (0: attend_kernel has it)
+  int nslot;    // partial results per row: the prefix's, then the cache's
+  int own_slot; // slot of the cache's first split
+  int own_rows; // ceil(G / 16)
+  bool direct;  // the only part: write O and lse
+  float scale_log2;
+  int64_t q_seq;
+  float* o_part;    // [nslot, B * Hq, D]
+  float* lse_part;  // [nslot, B * Hq] log2
+  float* score;     // [B, Hkv, G, cap] log2 units, or null
+  void* O;
+  float* lse;
+  float* weights;
+};
+
 template <typename T, int D>
-__global__ void __launch_bounds__(128) step_rows_kernel(StepArgs a, float* lse_out) {
-  const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (row >= (long long)a.B * a.Hq) return;
-  const int b = (int)(row / a.Hq), h = (int)(row % a.Hq), hk = h / a.G;
-  const int n = live_slots(a.lens, b, a.cap);
-  const T* q = static_cast<const T*>(a.Q) + b * a.q_seq + h * D;
-  float qf[D / 32], o[D / 32];
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e) {
-    qf[e] = to_f32(q[lane + 32 * e]);
-    o[e] = 0.f;
+__global__ void __launch_bounds__(kRowsThreads, 2)
+    rows_kernel(RowsArgs a, const __grid_constant__ CUtensorMap tmap_kp, const __grid_constant__ CUtensorMap tmap_vp,
+                const __grid_constant__ CUtensorMap tmap_kc, const __grid_constant__ CUtensorMap tmap_vc) {
+  using L = RowsSmem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* ml = reinterpret_cast<float*>(smem + L::kMl);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBars);
+  uint64_t* empty = full + L::kStages;
+  volatile int* abort_flag = reinterpret_cast<int*>(smem + L::kMisc);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // ---- which rows, which keys
+  int idx = blockIdx.x, hk, b0, rows, row0, n, split, nsplit, slot, z;
+  const bool pre = idx < a.npre * a.Hkv;
+  if (pre) {
+    hk = idx % a.Hkv;
+    split = idx / a.Hkv;
+    nsplit = a.npre;
+    b0 = 0;
+    row0 = 0;
+    rows = a.B * a.G;
+    n = a.P;
+    slot = split;
+    z = hk;
+  } else {
+    idx -= a.npre * a.Hkv;
+    hk = idx % a.Hkv;
+    idx /= a.Hkv;
+    b0 = idx % a.B;
+    idx /= a.B;
+    row0 = idx % a.own_rows * 16;
+    split = idx / a.own_rows;
+    nsplit = a.nown;
+    rows = a.G;
+    n = live_slots(a.lens, b0, a.cap);
+    slot = a.own_slot + split;
+    z = b0 * a.Hkv + hk;
   }
-  float m = -INFINITY, l = 0.f;
-  for (int part = 0; part < 2; ++part) {
-    const size_t off = part ? ((size_t)b * a.Hkv + hk) * a.cap * D : (size_t)hk * a.prefix_head;
-    const T* k = static_cast<const T*>(part ? a.Kc : a.Kp) + off;
-    const T* v = static_cast<const T*>(part ? a.Vc : a.Vp) + off;
-    const int keys = part ? n : a.P;
-    for (int j = 0; j < keys; ++j) {
-      float x = 0.f;
+  const int ntile = (n + kRowsKeys - 1) / kRowsKeys;
+  const int t0 = (int)((long long)ntile * split / nsplit), t1 = (int)((long long)ntile * (split + 1) / nsplit);
+  const int nt = t1 - t0;
+
+  if (tid == 0) {
+    for (int i = 0; i < L::kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 4);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const uint32_t ring = smem_u32(smem + L::kRing);
+
+  if (warp == 4) {
+    // ================================================================ loader
+    for (int i = 0; i < nt; ++i) {
+      const int st = i % L::kStages;
+      if (i >= L::kStages && !mbar_wait_warp(&empty[st], (i / L::kStages - 1) & 1, abort_flag)) break;
+      if (lane == 0) {
+        const uint32_t dst = ring + st * 2 * L::kTileBytes;
+        mbar_arrive_expect_tx(&full[st], 2 * L::kTileBytes);
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_3d(dst + c * kRowsKeys * 128, pre ? &tmap_kp : &tmap_kc, 64 * c, (t0 + i) * kRowsKeys, z, &full[st]);
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_3d(dst + L::kTileBytes + c * kRowsKeys * 128, pre ? &tmap_vp : &tmap_vc, 64 * c,
+                      (t0 + i) * kRowsKeys, z, &full[st]);
+      }
+    }
+    for (int i = max(0, nt - L::kStages); i < nt; ++i)  // no copy in flight is left behind
+      if (!mbar_wait_warp(&full[i % L::kStages], (i / L::kStages) & 1, abort_flag)) break;
+    return;
+  }
+
+  // ------------------------------------------------- 16 rows x 16 keys a tile
+  const int ra = row0 + (lane >> 2), rb = ra + 8;  // this lane's rows
+  auto q_row = [&](int r) -> const T* {
+    return static_cast<const T*>(a.Q) + (int64_t)(b0 + r / a.G) * a.q_seq + (int64_t)(hk * a.G + r % a.G) * D;
+  };
+  uint32_t q[D / 16][4];
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) x = fmaf(qf[e], to_f32(k[(size_t)j * D + lane + 32 * e]), x);
-      x = warp_sum(x) * a.scale_log2;
-      const float mn = fmaxf(m, x);
-      const float base = mn == -INFINITY ? 0.f : mn;
-      const float alpha = exp2f(m - base), p = exp2f(x - base);
-      l = l * alpha + p;
+  for (int k = 0; k < D / 16; ++k) {
+    const int c = 16 * k + (lane & 3) * 2;
+    q[k][0] = ra < rows ? *reinterpret_cast<const uint32_t*>(q_row(ra) + c) : 0u;
+    q[k][1] = rb < rows ? *reinterpret_cast<const uint32_t*>(q_row(rb) + c) : 0u;
+    q[k][2] = ra < rows ? *reinterpret_cast<const uint32_t*>(q_row(ra) + c + 8) : 0u;
+    q[k][3] = rb < rows ? *reinterpret_cast<const uint32_t*>(q_row(rb) + c + 8) : 0u;
+  }
+  float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) o[e] = o[e] * alpha + p * to_f32(v[(size_t)j * D + lane + 32 * e]);
-      m = mn;
+  for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+  const int key_k = 16 * warp + (lane >> 4) * 8 + (lane & 7), chunk_k = (lane >> 3) & 1;  // ldmatrix rows of K
+  const int key_v = 16 * warp + ((lane >> 3) & 1) * 8 + (lane & 7), chunk_v = lane >> 4;  // and of V
+  bool ok = true;
+  for (int i = 0; i < nt; ++i) {
+    const int st = i % L::kStages;
+    if (!mbar_wait_warp(&full[st], (i / L::kStages) & 1, abort_flag)) {
+      ok = false;
+      break;
+    }
+    const uint32_t ks = ring + st * 2 * L::kTileBytes, vs = ks + L::kTileBytes;
+    float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      uint32_t b[4];
+      const int ch = 2 * k + chunk_k;
+      ldmatrix_x4(ks + (ch >> 3) * (kRowsKeys * 128) + sw128_offset(key_k, ch & 7), b);
+      mma_16816<T>(s[0], q[k], b[0], b[1]);
+      mma_16816<T>(s[1], q[k], b[2], b[3]);
+    }
+    const int key0 = (t0 + i) * kRowsKeys + 16 * warp;  // the warp's first key
+    const int lim = n - key0;                           // keys that exist
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        s[h][e] = 8 * h + (lane & 3) * 2 + (e & 1) < lim ? s[h][e] * a.scale_log2 : -INFINITY;
+    if (!pre && a.score) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = e < 2 ? ra : rb;
+        float* dst = a.score + ((size_t)z * a.G + r) * a.cap + key0 + (lane & 3) * 2 + (e & 1);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (r < rows && 8 * h + (lane & 3) * 2 + (e & 1) < lim) dst[8 * h] = s[h][e];
+      }
+    }
+    if (lim < 16) {  // V rows behind the end may hold anything: 0 * NaN would reach every row
+      for (int x = lane; x < 16 * (D / 8); x += 32) {
+        const int row = x / (D / 8), ch = x % (D / 8);
+        if (row >= lim) st_shared_v4(vs + (ch >> 3) * (kRowsKeys * 128) + (16 * warp + row) * 128 + (ch & 7) * 16, 0u, 0u, 0u, 0u);
+      }
+      __syncwarp();
+    }
+    float alpha[2];
+    bool moved = false;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // rows ra, rb
+      float top = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const float mn = fmaxf(m[h], top);
+      const float base = mn == -INFINITY ? 0.f : mn;  // no key so far
+      alpha[h] = ex2_approx(m[h] - base);
+      moved |= mn > m[h];
+      m[h] = mn;
+      float sum = 0.f;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          s[t][2 * h + e] = ex2_approx(s[t][2 * h + e] - base);
+          sum += s[t][2 * h + e];
+        }
+      l[h] = l[h] * alpha[h] + sum;
+    }
+    if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+      for (int d = 0; d < D / 8; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[d][e] *= alpha[e >> 1];
+    }
+    const uint32_t p[4] = {pack16<T>(s[0][0], s[0][1]), pack16<T>(s[0][2], s[0][3]), pack16<T>(s[1][0], s[1][1]),
+                           pack16<T>(s[1][2], s[1][3])};
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) {
+      uint32_t b[4];
+      const int ch = 2 * d + chunk_v;
+      ldmatrix_x4_trans(vs + (ch >> 3) * (kRowsKeys * 128) + sw128_offset(key_v, ch & 7), b);
+      mma_16816<T>(o[2 * d], p, b[0], b[1]);
+      mma_16816<T>(o[2 * d + 1], p, b[2], b[3]);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[st]);
+  }
+  // ---- join the four warps
+  if (!ok && lane == 0) *abort_flag = 1;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+    if ((lane & 3) == 0) {
+      ml[warp * 16 + (lane >> 2) + 8 * h] = m[h];
+      ml[64 + warp * 16 + (lane >> 2) + 8 * h] = l[h];
     }
   }
-  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-  T* dst = static_cast<T*>(a.O) + (size_t)row * D;
+  named_bar_sync(1, 128);  // every warp is done with the ring
+  float* ow = reinterpret_cast<float*>(smem + L::kRing);  // [4][16][D]
+  {
+    float w[2];
 #pragma unroll
-  for (int e = 0; e < D / 32; ++e) dst[lane + 32 * e] = from_f32<T>(o[e] * inv);
-  if (lane == 0) {
-    const float lse = (m + log2f(l)) * kLn2;
-    if (a.lse) a.lse[row] = lse;
-    if (lse_out) lse_out[row] = lse;
+    for (int h = 0; h < 2; ++h) {
+      const int r = (lane >> 2) + 8 * h;
+      const float top = fmaxf(fmaxf(ml[r], ml[16 + r]), fmaxf(ml[32 + r], ml[48 + r]));
+      w[h] = m[h] == -INFINITY ? 0.f : ex2_approx(m[h] - top);
+    }
+#pragma unroll
+    for (int d = 0; d < D / 8; ++d)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<float2*>(ow + (warp * 16 + (lane >> 2) + 8 * h) * D + 8 * d + (lane & 3) * 2) =
+            make_float2(o[d][2 * h] * w[h], o[d][2 * h + 1] * w[h]);
+  }
+  named_bar_sync(1, 128);
+  if (*abort_flag) return;
+  for (int x = tid; x < 16 * (D / 4); x += 128) {
+    const int r = x / (D / 4), c = x % (D / 4) * 4;
+    if (row0 + r >= rows) break;
+    float top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) top = fmaxf(top, ml[16 * w + r]);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) sum += top == -INFINITY ? 0.f : ml[64 + 16 * w + r] * ex2_approx(ml[16 * w + r] - top);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float4 y = *reinterpret_cast<const float4*>(ow + (16 * w + r) * D + c);
+      v.x += y.x;
+      v.y += y.y;
+      v.z += y.z;
+      v.w += y.w;
+    }
+    v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+    const float lse2 = sum == 0.f ? -INFINITY : top + log2f(sum);
+    const size_t row = (size_t)(b0 + (row0 + r) / a.G) * a.Hq + hk * a.G + (row0 + r) % a.G;
+    if (a.direct) {
+      *reinterpret_cast<uint2*>(static_cast<T*>(a.O) + row * D + c) =
+          make_uint2(pack16<T>(v.x, v.y), pack16<T>(v.z, v.w));
+      if (c == 0 && a.lse) a.lse[row] = lse2 * kLn2;
+    } else {
+      *reinterpret_cast<float4*>(a.o_part + ((size_t)slot * a.B * a.Hq + row) * D + c) = v;
+      if (c == 0) a.lse_part[(size_t)slot * a.B * a.Hq + row] = lse2;
+    }
   }
 }
 
+// Joins the parts of the G rows of one (sequence, key/value head) and adds the
+// weights of kFinishKeys of its own keys.
 template <typename T, int D>
-__global__ void __launch_bounds__(128) step_weights_kernel(StepArgs a, const float* lse) {
-  const int bh = blockIdx.y, b = bh / a.Hkv, hk = bh % a.Hkv;
-  const int n = live_slots(a.lens, b, a.cap);
-  const int j = blockIdx.x * 128 + threadIdx.x;
-  if (j >= n) return;
-  const T* k = static_cast<const T*>(a.Kc) + ((size_t)bh * a.cap + j) * D;
-  float w = 0.f;
-  for (int g = 0; g < a.G; ++g) {
-    const int h = hk * a.G + g;
-    const T* q = static_cast<const T*>(a.Q) + b * a.q_seq + h * D;
-    float x = 0.f;
-    for (int e = 0; e < D; ++e) x = fmaf(to_f32(q[e]), to_f32(k[e]), x);
-    w += exp2f(x * a.scale_log2 - lse[b * a.Hq + h] * kLog2E);
+__global__ void __launch_bounds__(256) finish_kernel(RowsArgs a) {
+  extern __shared__ float lse2[];  // [G]
+  const int bh = blockIdx.x, b = bh / a.Hkv, hk = bh % a.Hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const size_t rows = (size_t)a.B * a.Hq, row0 = (size_t)b * a.Hq + hk * a.G;
+  const int n = a.weights ? live_slots(a.lens, b, a.cap) : 0;
+  if (blockIdx.y > 0 && (int)blockIdx.y * kFinishKeys >= n) return;
+  for (int g = warp; g < a.G; g += 8) {
+    float top = -INFINITY, sum = 0.f;
+    for (int i = lane; i < a.nslot; i += 32) top = fmaxf(top, a.lse_part[i * rows + row0 + g]);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    for (int i = lane; i < a.nslot; i += 32)
+      sum += top == -INFINITY ? 0.f : exp2f(a.lse_part[i * rows + row0 + g] - top);
+    sum = warp_sum(sum);
+    const float y = sum == 0.f ? -INFINITY : top + log2f(sum);
+    if (lane == 0) lse2[g] = y;
+    if (blockIdx.y > 0) continue;
+    if (lane == 0 && a.lse) a.lse[row0 + g] = y * kLn2;
+    float o[D / 32];
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < a.nslot; ++i) {
+      const float x = a.lse_part[i * rows + row0 + g];
+      if (x == -INFINITY) continue;  // an empty part's rows were not written
+      const float w = exp2f(x - y);
+      const float* src = a.o_part + (i * rows + row0 + g) * D;
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) o[e] = fmaf(w, src[lane + 32 * e], o[e]);
+    }
+    T* dst = static_cast<T*>(a.O) + (row0 + g) * D;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) dst[lane + 32 * e] = from_f32<T>(o[e]);
   }
-  a.weights[(size_t)bh * a.cap + j] += w;
+  if (!a.weights) return;
+  __syncthreads();
+  const int j1 = min(n, (int)(blockIdx.y + 1) * kFinishKeys);
+  const float* score = a.score + (size_t)bh * a.G * a.cap;
+  float* w = a.weights + (size_t)bh * a.cap;
+  for (int j = blockIdx.y * kFinishKeys + threadIdx.x; j < j1; j += 256) {
+    float sum = 0.f;
+    for (int g = 0; g < a.G; ++g) sum += ex2_approx(score[(size_t)g * a.cap + j] - lse2[g]);
+    w[j] += sum;
+  }
+}
+
+namespace {
+struct StepPlan {
+  int nown, npre_rows, npre_tc;
+  bool direct;
+  size_t o_part, lse_part, score, total;
+};
+
+StepPlan step_plan(const StepArgs& a, bool with_weights) {
+  StepPlan p{};
+  const int own_rows = (a.G + 15) / 16;
+  // own: enough CTAs for a few waves of two per SM, at least 8 tiles each
+  const long long ctas = (long long)a.B * a.Hkv * own_rows;
+  long long n = (8 * kSms + ctas - 1) / ctas;
+  if (n > a.cap / 512) n = a.cap / 512;
+  if (n > 64) n = 64;
+  p.nown = a.cap == 0 ? 0 : n < 1 ? 1 : (int)n;
+  if (a.P > 0) {
+    if (a.B * a.G <= 16) {
+      n = (4 * kSms + a.Hkv - 1) / a.Hkv;
+      if (n > a.P / 256) n = a.P / 256;
+      if (n > 64) n = 64;
+      p.npre_rows = n < 1 ? 1 : (int)n;
+    } else {
+      p.npre_tc = key_splits(row_pairs(a.B, a.G, 1) * a.Hkv, a.P);
+    }
+  }
+  const int nslot = p.nown + p.npre_rows + p.npre_tc;
+  p.direct = nslot <= 1 && p.npre_tc == 0 && !with_weights;
+  const size_t rows = (size_t)a.B * a.Hq;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  p.lse_part = p.direct ? 0 : up(rows * nslot * a.d * 4);
+  p.score = p.lse_part + (p.direct ? 0 : up(rows * nslot * 4));
+  p.total = p.score + (with_weights ? up(rows * a.cap * 4) : 0);
+  if (p.total < 256) p.total = 256;
+  return p;
 }
 
 template <typename T, int D>
-cudaError_t run(const StepArgs& a, cudaStream_t s) {
-  float* lse = a.weights ? static_cast<float*>(a.ws) : nullptr;
-  step_rows_kernel<T, D><<<(unsigned)(((long long)a.B * a.Hq + 3) / 4), 128, 0, s>>>(a, lse);
-  if (a.weights && a.cap)
-    step_weights_kernel<T, D><<<dim3((a.cap + 127) / 128, a.B * a.Hkv), 128, 0, s>>>(a, lse);
+cudaError_t run_step(const StepArgs& s, const StepPlan& p, cudaStream_t st) {
+  RowsArgs a{};
+  a.Q = s.Q;
+  a.lens = s.lens;
+  a.B = s.B;
+  a.Hq = s.Hq;
+  a.Hkv = s.Hkv;
+  a.G = s.G;
+  a.P = s.P;
+  a.cap = s.cap;
+  a.nown = p.nown;
+  a.npre = p.npre_rows;
+  a.nslot = p.nown + p.npre_rows + p.npre_tc;
+  a.own_slot = p.npre_rows + p.npre_tc;
+  a.own_rows = (s.G + 15) / 16;
+  a.direct = p.direct;
+  a.scale_log2 = s.scale_log2;
+  a.q_seq = s.q_seq;
+  char* ws = static_cast<char*>(s.ws);
+  a.o_part = reinterpret_cast<float*>(ws);
+  a.lse_part = reinterpret_cast<float*>(ws + p.lse_part);
+  a.score = s.weights ? reinterpret_cast<float*>(ws + p.score) : nullptr;
+  a.O = s.O;
+  a.lse = s.lse;
+  a.weights = s.weights;
+  cudaError_t e;
+  if (p.npre_tc) {
+    TcArgs t{};
+    t.Q = s.Q;
+    t.o_part = a.o_part;
+    t.lse_part = a.lse_part;
+    t.nseq = 1;
+    t.Hq = s.Hq;
+    t.Hkv = s.Hkv;
+    t.G = s.G;
+    t.Tq = s.B;
+    t.Tk = s.P;
+    t.nsplit = p.npre_tc;
+    t.ntile = (int)row_pairs(s.B, s.G, 1);
+    t.partial = true;
+    t.scale_log2 = s.scale_log2;
+    t.q_tok = s.q_seq;
+    t.q_head = D;
+    CUtensorMap tk, tv;
+    e = make_tmap_rows(&tk, s.Kp, s.dtype, D, s.P, s.Hkv, D, s.prefix_head);
+    if (e == cudaSuccess) e = make_tmap_rows(&tv, s.Vp, s.dtype, D, s.P, s.Hkv, D, s.prefix_head);
+    if (e == cudaSuccess) e = run_attend<T, D>(t, tk, tv, st);
+    if (e != cudaSuccess) return e;
+  }
+  const long long ctas =
+      (long long)a.npre * a.Hkv + (long long)a.nown * a.Hkv * a.B * a.own_rows;
+  if (ctas > 0) {
+    CUtensorMap kp, vp, kc, vc;
+    // a map that no CTA uses needs an address all the same
+    const bool pre = a.npre > 0, own = a.nown > 0;
+    e = make_tmap_rows(&kp, pre ? s.Kp : s.Q, s.dtype, D, pre ? s.P : 1, s.Hkv, D, pre ? s.prefix_head : D, kRowsKeys);
+    if (e == cudaSuccess)
+      e = make_tmap_rows(&vp, pre ? s.Vp : s.Q, s.dtype, D, pre ? s.P : 1, s.Hkv, D, pre ? s.prefix_head : D, kRowsKeys);
+    if (e == cudaSuccess)
+      e = make_tmap_rows(&kc, own ? s.Kc : s.Q, s.dtype, D, own ? s.cap : 1, s.B * s.Hkv, D,
+                         own ? (int64_t)s.cap * D : D, kRowsKeys);
+    if (e == cudaSuccess)
+      e = make_tmap_rows(&vc, own ? s.Vc : s.Q, s.dtype, D, own ? s.cap : 1, s.B * s.Hkv, D,
+                         own ? (int64_t)s.cap * D : D, kRowsKeys);
+    if (e != cudaSuccess) return e;
+    const size_t sm = RowsSmem<D>::bytes();
+    e = cudaFuncSetAttribute(rows_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+    if (e != cudaSuccess) return e;
+    rows_kernel<T, D><<<(unsigned)ctas, kRowsThreads, sm, st>>>(a, kp, vp, kc, vc);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  if (p.direct && ctas > 0) return cudaSuccess;
+  const dim3 grid(s.B * s.Hkv, s.weights ? (unsigned)max(1, (s.cap + kFinishKeys - 1) / kFinishKeys) : 1u);
+  finish_kernel<T, D><<<grid, 256, s.G * 4, st>>>(a);
   return cudaGetLastError();
 }
 }  // namespace
 
-size_t step_ws(const StepArgs& a, bool with_weights) {
-  return with_weights ? ((size_t)a.B * a.Hq * 4 + 255) / 256 * 256 : 256;
-}
+size_t step_ws(const StepArgs& a, bool with_weights) { return step_plan(a, with_weights).total; }
 
 cudaError_t launch_step(const StepArgs& a, cudaStream_t s) {
-  if (a.dtype == IG_BF16) return a.d == 128 ? run<__nv_bfloat16, 128>(a, s) : run<__nv_bfloat16, 64>(a, s);
-  return a.d == 128 ? run<__half, 128>(a, s) : run<__half, 64>(a, s);
+  const StepPlan p = step_plan(a, a.weights != nullptr);
+  if (a.dtype == IG_BF16)
+    return a.d == 128 ? run_step<__nv_bfloat16, 128>(a, p, s) : run_step<__nv_bfloat16, 64>(a, p, s);
+  return a.d == 128 ? run_step<__half, 128>(a, p, s) : run_step<__half, 64>(a, p, s);
 }
 
 }  // namespace ig
