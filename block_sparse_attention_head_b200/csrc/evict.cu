@@ -1,55 +1,43 @@
 // Eviction from the caches by accumulated attention weight (instagen_evict).
 //
-// Two launches.  evict_select_kernel, one CTA per (sequence, head): the slots
-// compete by (recent, weight, lower slot).  A radix select over the weights'
-// ordered bits, one byte per pass, finds the weight at the budget and how many
-// of the keys equal to it stay (the lowest slots); one ordered pass then lists
-// the freed slots below the budget and the kept slots from the budget on.
+// Two launches.  evict_select_kernel, one CTA per (sequence, head): every slot
+// gets a 32-bit key whose order is the order of eviction (recent, weight), and
+// a radix select finds the key at the budget and how many of the slots equal
+// to it stay (the lowest).  Weights and positions are read once into shared
+// memory (twice the positions: the recent ones are known once the newest is);
+// a pass counts one byte of the keys, lanes with equal bytes adding together,
+// because weights share their exponents.  Then each warp walks a contiguous
+// range of slots and, from the counts of the ranges before, lists the freed
+// slots below the budget and the kept slots from the budget on.
 // evict_move_kernel copies rows: the n-th of those into the n-th of these (in
-// place), or every kept row (into another cache).  Sources are at or above
-// the budget and destinations below it, so moving in place has no order.
+// place), or every kept row (into another cache); it is bound by the rows'
+// bytes.  Sources are at or above the budget and destinations below it, so
+// moving in place has no order.
 #include "serve.cuh"
 
 namespace ig {
 
 namespace {
-constexpr int kEvictThreads = 1024;
-constexpr int kEvictWarps = kEvictThreads / 32;
+constexpr int kEvictKeys = 49152;  // keys held in shared memory; longer caches are read again in every pass
 constexpr int kEvictMoveThreads = 256;
-constexpr int kEvictMoveRows = 32;  // rows per CTA of the move kernel
+constexpr int kEvictMoveRows = 4;  // rows a thread copies, all loads in flight at once
 
 // Ordered bits: a < b as numbers iff bits(a) < bits(b); -0 counts as +0, NaN
-// is below everything.
+// is 1, below everything.  0 and 2^32 - 1 are no number's.
 __device__ __forceinline__ uint32_t ordered_bits(float w) {
-  if (w != w) return 0u;
+  if (w != w) return 1u;
   const uint32_t u = __float_as_uint(w + 0.f);
   return (u >> 31) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive prefix sum of v over the block's threads; *total gets the sum.
-__device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  __syncthreads();  // warp_sums may still be read by the last scan
-  if (lane == 31) warp_sums[warp] = x;
+// Exclusive prefix sum over the block's warps of a value that each warp's
+// lanes share.
+__device__ __forceinline__ int warps_before(int v, int* sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  __syncthreads();  // sums may still be read by the last call
+  if (lane == 0) sums[warp] = v;
   __syncthreads();
-  if (warp == 0) {
-    int s = warp_sums[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += y;
-    }
-    warp_sums[lane] = s;
-  }
-  __syncthreads();
-  *total = warp_sums[kEvictWarps - 1];
-  return x - v + (warp ? warp_sums[warp - 1] : 0);
+  return __reduce_add_sync(0xffffffffu, lane < warp && lane < nw ? sums[lane] : 0);
 }
 
 struct EvictLists {
@@ -68,13 +56,16 @@ __host__ __device__ inline EvictLists carve(void* ws, int B, int Hkv, int budget
   return l;
 }
 
-__global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(EvictArgs a) {
+// kHeld: the keys fit shared memory.
+template <bool kHeld>
+__global__ void __launch_bounds__(1024) evict_select_kernel(EvictArgs a) {
+  extern __shared__ uint32_t held[];
   __shared__ int hist[256];
-  __shared__ int warp_sums[kEvictWarps];
+  __shared__ int sums[32];
   __shared__ uint32_t s_prefix;
-  __shared__ int s_need, s_newest, s_safe;
-  const int bh = blockIdx.x, b = bh / a.Hkv;
-  const int tid = threadIdx.x, lane = tid & 31;
+  __shared__ int s_need, s_equal, s_newest, s_safe;
+  const int bh = blockIdx.x, b = bh / a.Hkv, nt = blockDim.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const EvictLists l = carve(a.ws, a.B, a.Hkv, a.budget);
   const int n = live_slots(a.lens, b, a.cap);
   if (tid == 0 && bh % a.Hkv == 0) l.n[b] = n;
@@ -82,7 +73,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(EvictArgs a
   int32_t* src = l.src + (size_t)bh * a.budget;
   if (n <= a.budget) {  // everything stays
     if (!a.in_place)
-      for (int i = tid; i < n; i += kEvictThreads) src[i] = i;
+      for (int i = tid; i < n; i += nt) src[i] = i;
     if (tid == 0) l.count[bh] = a.in_place ? 0 : n;
     return;
   }
@@ -91,44 +82,57 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(EvictArgs a
 
   // the recent slots: pos > newest - recent
   int newest = INT32_MIN;
-  for (int i = tid; i < n; i += kEvictThreads) newest = max(newest, pos[i]);
+#pragma unroll 8
+  for (int i = tid; i < n; i += nt) newest = max(newest, pos[i]);
   newest = __reduce_max_sync(0xffffffffu, newest);
   if (tid == 0) {
     s_newest = INT32_MIN;
     s_safe = 0;
+    s_need = a.budget;
+    s_prefix = 0;
   }
   __syncthreads();
   if (lane == 0) atomicMax(&s_newest, newest);
   __syncthreads();
   const long long edge = (long long)s_newest - a.recent;
   int safe = 0;
-  for (int i = tid; i < n; i += kEvictThreads) safe += pos[i] > edge;
+#pragma unroll 8
+  for (int i = tid; i < n; i += nt) safe += pos[i] > edge;
   safe = __reduce_add_sync(0xffffffffu, safe);
   if (lane == 0) atomicAdd(&s_safe, safe);
   __syncthreads();
-  // either the recent slots alone compete (there are enough of them), or all
-  // of them stay and the others compete for what is left of the budget
+  // either there are enough recent slots and the others are below all of
+  // them, or the recent ones are above all others
   const bool among_safe = s_safe >= a.budget;
-  if (tid == 0) {
-    s_need = among_safe ? a.budget : a.budget - s_safe;
-    s_prefix = 0;
+  auto read_key = [&](int i) -> uint32_t {
+    const uint32_t key = ordered_bits(w[i]);
+    return (pos[i] > edge) == among_safe ? key : among_safe ? 0u : 0xffffffffu;
+  };
+  if (kHeld) {
+#pragma unroll 8
+    for (int i = tid; i < n; i += nt) held[i] = read_key(i);
+    __syncthreads();
   }
-  __syncthreads();
-  auto competes = [&](int i) { return (pos[i] > edge) == among_safe; };
+  auto key_at = [&](int i) -> uint32_t { return kHeld ? held[i] : read_key(i); };
 
-  // radix select: after a pass, s_prefix holds the leading bytes of the
-  // weight at the budget and s_need how many of the slots sharing them stay
+  // radix select: after a pass, s_prefix holds the leading bytes of the key
+  // at the budget, s_equal how many slots share them and s_need how many of
+  // those stay; done when all of them do
   uint32_t mask = 0;
   for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0;
+    for (int i = tid; i < 256; i += nt) hist[i] = 0;
     __syncthreads();
     const uint32_t prefix = s_prefix;
-    for (int i = tid; i < n; i += kEvictThreads) {
-      const uint32_t key = ordered_bits(w[i]);
-      if (competes(i) && (key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255], 1);
+    for (int i0 = warp * 32; i0 < n; i0 += nt) {
+      const int i = i0 + lane;
+      const uint32_t key = i < n ? key_at(i) : 0u;
+      const bool in = i < n && (key & mask) == prefix;
+      const int digit = in ? (int)((key >> shift) & 255) : 256;
+      const unsigned peers = __match_any_sync(0xffffffffu, digit);
+      if (in && lane == __ffs(peers) - 1) atomicAdd(&hist[digit], __popc(peers));
     }
     __syncthreads();
-    if (tid < 32) {  // the largest byte whose suffix count reaches need
+    if (warp == 0) {  // the largest byte whose count from above reaches need
       int own = 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) own += hist[255 - (8 * lane + e)];
@@ -147,6 +151,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(EvictArgs a
           if (run + hist[byte] >= need) {
             s_prefix = prefix | ((uint32_t)byte << shift);
             s_need = need - run;
+            s_equal = hist[byte];
             break;
           }
           run += hist[byte];
@@ -155,58 +160,74 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(EvictArgs a
     }
     mask |= 255u << shift;
     __syncthreads();
+    if (s_need == s_equal) break;
   }
   const uint32_t level = s_prefix;
   const int equal_kept = s_need;
+  const bool all_equal = s_need == s_equal;
 
-  // ordered pass: every thread owns a contiguous run of slots
-  const int run_len = (n + kEvictThreads - 1) / kEvictThreads;
-  const int i0 = min(n, tid * run_len), i1 = min(n, i0 + run_len);
-  int equal = 0, total;
-  for (int i = i0; i < i1; ++i) equal += competes(i) && ordered_bits(w[i]) == level;
-  const int equal_before = block_scan(equal, warp_sums, &total);
+  // ordered walk: every warp owns a contiguous range of slots
+  const int nw = nt >> 5, seg = (n + 32 * nw - 1) / (32 * nw) * 32;
+  const int i0 = min(n, warp * seg), i1 = min(n, i0 + seg);
+  const unsigned below = (1u << lane) - 1;
+  int equal_before = 0;
+  if (!all_equal) {
+    int equal = 0;
+    for (int i = i0 + lane; i < i1; i += 32) equal += (key_at(i) & mask) == level;
+    equal_before = warps_before(__reduce_add_sync(0xffffffffu, equal), sums);
+  }
+  // f(slot, below the budget and freed, from the budget on and kept) for the
+  // range's slots, 32 at a time
   auto each = [&](auto f) {
     int eq = equal_before;
-    for (int i = i0; i < i1; ++i) {
-      bool kept;
-      if (competes(i)) {
-        const uint32_t key = ordered_bits(w[i]);
-        kept = key > level || (key == level && eq < equal_kept);
-        eq += key == level;
+    for (int i = i0 + lane; i - lane < i1; i += 32) {
+      const uint32_t key = i < i1 ? key_at(i) & mask : 0u;
+      bool kept = key > level;
+      if (all_equal) {
+        kept = key >= level;
       } else {
-        kept = !among_safe;
+        const unsigned same = __ballot_sync(0xffffffffu, i < i1 && key == level);
+        if (key == level) kept = eq + __popc(same & below) < equal_kept;
+        eq += __popc(same);
       }
-      f(i, kept);
+      f(i, i < i1 && !kept && i < a.budget, i < i1 && kept && i >= a.budget);
     }
   };
   int freed = 0, moving = 0;
-  each([&](int i, bool kept) {
-    freed += i < a.budget && !kept;
-    moving += i >= a.budget && kept;
+  each([&](int, bool free, bool moves) {
+    freed += __popc(__ballot_sync(0xffffffffu, free));
+    moving += __popc(__ballot_sync(0xffffffffu, moves));
   });
-  int count, count2;
-  int f = block_scan(freed, warp_sums, &count);
-  int m = block_scan(moving, warp_sums, &count2);
-  int32_t* from = a.in_place ? src : dst;  // out of place: dst is the list of the moving slots first
-  each([&](int i, bool kept) {
-    if (i >= a.budget && kept) from[m++] = i;
-  });
-  __syncthreads();
-  each([&](int i, bool kept) {
-    if (i < a.budget) {
-      if (a.in_place) {
-        if (!kept) dst[f++] = i;
-      } else {
-        src[i] = kept ? i : from[f++];
-      }
-    }
-  });
-  if (tid == 0) l.count[bh] = a.in_place ? count : a.budget;
+  int f = warps_before(freed, sums), m = warps_before(moving, sums);
+  if (warp == nw - 1 && lane == 0) l.count[bh] = a.in_place ? f + freed : a.budget;
+  int32_t* from = a.in_place ? src : dst;  // out of place: dst is the list of the moving slots
+  if (a.in_place) {
+    each([&](int i, bool free, bool moves) {
+      const unsigned fs = __ballot_sync(0xffffffffu, free), ms = __ballot_sync(0xffffffffu, moves);
+      if (free) dst[f + __popc(fs & below)] = i;
+      if (moves) src[m + __popc(ms & below)] = i;
+      f += __popc(fs);
+      m += __popc(ms);
+    });
+  } else {
+    each([&](int i, bool, bool moves) {
+      const unsigned ms = __ballot_sync(0xffffffffu, moves);
+      if (moves) from[m + __popc(ms & below)] = i;
+      m += __popc(ms);
+    });
+    __syncthreads();
+    each([&](int i, bool free, bool) {
+      const unsigned fs = __ballot_sync(0xffffffffu, free);
+      if (i < i1 && i < a.budget) src[i] = free ? from[f + __popc(fs & below)] : i;
+      f += __popc(fs);
+    });
+  }
 }
 
 template <int D>
 __global__ void __launch_bounds__(kEvictMoveThreads) evict_move_kernel(EvictArgs a) {
-  constexpr int kLanes = D / 8;  // 16-byte chunks of a row
+  constexpr int kLanes = D / 8;                        // 16-byte chunks of a row
+  constexpr int kGroup = kEvictMoveThreads / kLanes;   // rows at once
   const int bh = blockIdx.y, b = bh / a.Hkv;
   const EvictLists l = carve(a.ws, a.B, a.Hkv, a.budget);
   const int count = l.count[bh];
@@ -214,17 +235,32 @@ __global__ void __launch_bounds__(kEvictMoveThreads) evict_move_kernel(EvictArgs
   const int32_t* dst = l.dst + (size_t)bh * a.budget;
   const int32_t* src = l.src + (size_t)bh * a.budget;
   const size_t in0 = (size_t)bh * a.cap, out0 = (size_t)bh * a.cap_out;
-  const int c = threadIdx.x % kLanes;
-  const int end = min(count, (int)(blockIdx.x + 1) * kEvictMoveRows);
-  for (int r = blockIdx.x * kEvictMoveRows + threadIdx.x / kLanes; r < end; r += kEvictMoveThreads / kLanes) {
-    const size_t from = in0 + src[r], to = out0 + (a.in_place ? dst[r] : r);
-    const uint4 k = static_cast<const uint4*>(a.K)[from * kLanes + c];
-    const uint4 v = static_cast<const uint4*>(a.V)[from * kLanes + c];
-    static_cast<uint4*>(a.K_out)[to * kLanes + c] = k;
-    static_cast<uint4*>(a.V_out)[to * kLanes + c] = v;
+  const int c = threadIdx.x % kLanes, r0 = blockIdx.x * (kGroup * kEvictMoveRows) + threadIdx.x / kLanes;
+  uint4 k[kEvictMoveRows], v[kEvictMoveRows];
+  float w[kEvictMoveRows];
+  int32_t p[kEvictMoveRows];
+#pragma unroll
+  for (int e = 0; e < kEvictMoveRows; ++e) {
+    const int r = r0 + e * kGroup;
+    if (r >= count) break;
+    const size_t from = in0 + src[r];
+    k[e] = static_cast<const uint4*>(a.K)[from * kLanes + c];
+    v[e] = static_cast<const uint4*>(a.V)[from * kLanes + c];
     if (c == 0) {
-      a.weights_out[to] = a.weights[from];
-      a.pos_out[to] = a.pos[from];
+      w[e] = a.weights[from];
+      p[e] = a.pos[from];
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < kEvictMoveRows; ++e) {
+    const int r = r0 + e * kGroup;
+    if (r >= count) break;
+    const size_t to = out0 + (a.in_place ? dst[r] : r);
+    static_cast<uint4*>(a.K_out)[to * kLanes + c] = k[e];
+    static_cast<uint4*>(a.V_out)[to * kLanes + c] = v[e];
+    if (c == 0) {
+      a.weights_out[to] = w[e];
+      a.pos_out[to] = p[e];
     }
   }
 }
@@ -235,11 +271,21 @@ size_t evict_ws(int B, int Hkv, int budget) {
 }
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
-  evict_select_kernel<<<a.B * a.Hkv, kEvictThreads, 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
+  // short caches: several CTAs per SM; long ones: all of an SM's threads
+  const int threads = a.cap <= 4096 ? 256 : 1024;
+  cudaError_t e = cudaSuccess;
+  if (a.cap <= kEvictKeys) {
+    e = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvictKeys * 4);
+    if (e != cudaSuccess) return e;
+    evict_select_kernel<true><<<a.B * a.Hkv, threads, (size_t)a.cap * 4, s>>>(a);
+  } else {
+    evict_select_kernel<false><<<a.B * a.Hkv, threads, 0, s>>>(a);
+  }
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int rows = a.in_place ? min(a.budget, a.cap - a.budget) : a.budget;
-  const dim3 grid((unsigned)max(1, (rows + kEvictMoveRows - 1) / kEvictMoveRows), (unsigned)(a.B * a.Hkv));
+  const int per_cta = kEvictMoveThreads / (a.d / 8) * kEvictMoveRows;
+  const dim3 grid((unsigned)max(1, (rows + per_cta - 1) / per_cta), (unsigned)(a.B * a.Hkv));
   if (a.d == 128)
     evict_move_kernel<128><<<grid, kEvictMoveThreads, 0, s>>>(a);
   else
