@@ -14,7 +14,8 @@
 //
 // Bound: the exponentials, 2 * 2048 MUFU cycles per tile and CTA against 2 *
 // 1024 tensor cycles (d = 128); three eighths of those of unmasked tiles run
-// on the FMA pipe instead (degree 5: the sums keep fp32's digits).
+// on the FMA pipe instead (degree 5: the sums keep fp32's digits).  Sixteen
+// warps share them, four per scheduler, two to a TMEM lane.
 //
 // Few keys, many queries: nsplit CTAs share a key pair, each over its part of
 // the tiles, and add_parts_kernel adds their sums in order.
@@ -23,7 +24,7 @@
 namespace ig {
 
 namespace {
-constexpr int kKwThreads = 384;
+constexpr int kKwThreads = 640;  // 16 warps of sums, 2 MMA, loader, lse
 constexpr int kKwTile = 256;   // keys per CTA, queries per tile
 constexpr int kKwLseRing = 4;
 
@@ -34,7 +35,8 @@ struct KwSmem {
   static constexpr int kK = 0;
   static constexpr int kQ = kK + 2 * kKeyBytes;
   static constexpr int kLse = kQ + 2 * kQBytes;
-  static constexpr int kBars = kLse + kKwLseRing * kKwTile * 4;
+  static constexpr int kXch = kLse + kKwLseRing * kKwTile * 4;  // the second half rows' sums
+  static constexpr int kBars = kXch + 256 * 4;
   static constexpr int kMisc = kBars + 24 * 8;
   static constexpr int kBytes = kMisc + 64;
   static constexpr size_t bytes() { return 1024 + kBytes; }
@@ -60,6 +62,7 @@ __global__ void __launch_bounds__(kKwThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* nlse = reinterpret_cast<float*>(smem + L::kLse);
+  float* xch = reinterpret_cast<float*>(smem + L::kXch);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
   uint64_t* k_full = bars + 0;
   uint64_t* q_full = bars + 1;   // [2] stages
@@ -109,17 +112,17 @@ __global__ void __launch_bounds__(kKwThreads, 1)
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 2);
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 128);
+      mbar_init(&s_empty[i], 256);
       mbar_init(&fin[i], 1);
     }
     for (int i = 0; i < kKwLseRing; ++i) {
       mbar_init(&l_full[i], 32);
-      mbar_init(&l_empty[i], 256);
+      mbar_init(&l_empty[i], 512);
     }
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 8) {
+  if (warp == 16) {
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
   }
@@ -129,7 +132,8 @@ __global__ void __launch_bounds__(kKwThreads, 1)
   const uint32_t tmem = *tmem_holder;
   const uint32_t k_s = smem_u32(smem + L::kK), q_s = smem_u32(smem + L::kQ);
 
-  if (warp == 10) {
+  float acc = 0.f;
+  if (warp == 18) {
     // ================================================================ loader
     if (lane == 0 && nv > 0) {
       mbar_arrive_expect_tx(k_full, 2 * L::kKeyBytes);
@@ -151,7 +155,7 @@ __global__ void __launch_bounds__(kKwThreads, 1)
     }
     if (nv > 0) mbar_wait_drain(k_full, 0);  // no copy in flight is left behind
     for (int i = max(0, issued - 2); i < issued; ++i) mbar_wait_drain(&q_full[i & 1], (i >> 1) & 1);
-  } else if (warp == 11) {
+  } else if (warp == 19) {
     // =================================================================== lse
     for (int i = 0; i < nv; ++i) {
       const int st = i % kKwLseRing, v = v0 + i;
@@ -168,9 +172,9 @@ __global__ void __launch_bounds__(kKwThreads, 1)
       for (int e = 0; e < 8; ++e) nlse[st * kKwTile + lane + 32 * e] = x[e];
       mbar_arrive(&l_full[st]);
     }
-  } else if (warp >= 8) {
+  } else if (warp >= 16) {
     // =================================================================== MMA
-    const int t = warp - 8;
+    const int t = warp - 16;
     const uint32_t idesc = umma_idesc_f16kind(128, 256, false, false, kHalf);
     const uint64_t kd = umma_desc_sw128(k_s + t * L::kKeyBytes, 16, 1024);
     const uint64_t qd0 = umma_desc_sw128(q_s, 16, 1024);
@@ -197,23 +201,21 @@ __global__ void __launch_bounds__(kKwThreads, 1)
     mbar_wait_drain(&fin[t], 0);
   } else {
     // ================================================================ sums
-    const int t = warp >> 2, qd = warp & 3;
+    // four warpgroups: chain t's lanes, columns [128 half, 128 half + 128)
+    const int t = warp >> 3, half = (warp >> 2) & 1, qd = warp & 3;
     const int key = kb + 128 * t + 32 * qd + lane;
-    const uint32_t s_col = tmem + (uint32_t)((32 * qd) << 16) + 256 * t;
+    const uint32_t s_col = tmem + (uint32_t)((32 * qd) << 16) + 256 * t + 128 * half;
     const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
-    float acc = 0.f;
     for (int i = 0; i < nv; ++i) {
-      const int tok = (i0 + (v0 + i) % ntile) * kKwTile;
-      // columns [lo, hi) of the tile: queries that exist and see this key
+      const int tok = (i0 + (v0 + i) % ntile) * kKwTile + 128 * half;
+      // columns [lo, hi) of the half tile: queries that exist and see this key
       const int lo = a.causal ? key - off - tok : 0, hi = nq - tok;
-      const bool whole = hi >= kKwTile && (!a.causal || kb + 128 * t + 127 - off <= tok);
-      const float* nl = nlse + (i % kKwLseRing) * kKwTile;
+      const bool whole = hi >= 128 && (!a.causal || kb + 128 * t + 127 - off <= tok);
+      const float* nl = nlse + (i % kKwLseRing) * kKwTile + 128 * half;
       if (!mbar_wait_warp(&l_full[i % kKwLseRing], (i / kKwLseRing) & 1, abort_flag)) break;
       if (!mbar_wait_warp(&s_full[t], i & 1, abort_flag)) break;
       tc_fence_after();
-      float x[2][32];
       uint64_t sum[2] = {0ull, 0ull};
-      tmem_ld32(s_col, x[0]);
       auto chunk = [&](int c, float (&v)[32], auto masked) {
         constexpr bool kMask = decltype(masked)::value;
 #pragma unroll
@@ -240,37 +242,42 @@ __global__ void __launch_bounds__(kKwThreads, 1)
           }
         }
       };
-#pragma unroll
-      for (int c = 0; c < kKwTile / 32; ++c) {
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        float x[32];
+        tmem_ld32(s_col + 32 * c, x);
         tmem_wait_ld();
-        pin_regs32(x[c & 1]);
-        if (c + 1 < kKwTile / 32) {
-          tmem_ld32(s_col + 32 * (c + 1), x[(c + 1) & 1]);
-        } else {
+        pin_regs32(x);
+        if (c == 3) {
           tc_fence_before();
           mbar_arrive(&s_empty[t]);
         }
         if (whole)
-          chunk(c, x[c & 1], std::false_type());
+          chunk(c, x, std::false_type());
         else
-          chunk(c, x[c & 1], std::true_type());
+          chunk(c, x, std::true_type());
       }
       mbar_arrive(&l_empty[i % kKwLseRing]);
       float s0, s1;
       unpack2(add2(sum[0], sum[1]), s0, s1);
       acc += s0 + s1;
     }
-    if (key < nk) {
-      const size_t at = (size_t)hk * a.Tk + k0s + key;
+    if (half == 1) xch[128 * t + 32 * qd + lane] = acc;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp < 16 && !((warp >> 2) & 1)) {
+    const int lane_t = 128 * (warp >> 3) + 32 * (warp & 3) + lane;
+    if (kb + lane_t < nk) {
+      const size_t at = (size_t)hk * a.Tk + k0s + kb + lane_t;
+      acc += xch[lane_t];
       if (a.nsplit > 1)
         a.parts[(size_t)z * a.Hkv * a.Tk + at] = acc;
       else
         a.weights[at] += acc;
     }
   }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 8) {
+  if (warp == 16) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

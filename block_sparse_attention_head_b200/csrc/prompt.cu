@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t* o_done = bars + 16;  // [2] chains
   uint64_t* fin = bars + 18;     // [2] chains
   uint64_t* v_fixed = bars + 20;
+  uint64_t* turn = bars + 21;    // [2] chains: may issue its next block of MMAs
   int* misc = reinterpret_cast<int*>(smem + L::kMisc);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(misc + 0);
   volatile int* abort_flag = misc + 1;
@@ -237,6 +238,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&p_tail[i], 128);
       mbar_init(&o_done[i], 1);
       mbar_init(&fin[i], 1);
+      mbar_init(&turn[i], 1);
     }
     mbar_init(v_fixed, 32);
     *abort_flag = 0;
@@ -304,11 +306,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int step = one ? 2 : 1, i0 = one ? t : 0;
       const int iend = (!one && t == 0 ? end0 : j1) - j0;
       bool ok = true;
+      // PV_t of tile i (the chain's ph-th), in two parts as P arrives
       auto issue_pv = [&](int i, int ph) -> bool {
-        if (!mbar_wait_warp(&v_full[i & 1], (i >> 1) & 1, abort_flag)) return false;
-        if (j0 + i == cut && !mbar_wait_warp(v_fixed, 0, abort_flag)) return false;
-        if (!mbar_wait_warp(&p_head[t], ph & 1, abort_flag)) return false;
-        tc_fence_after();
         const uint64_t vd = vd0 + (uint64_t)(i & 1) * kTileStep;
         if (elect_one()) {
 #pragma unroll
@@ -326,9 +325,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         __syncwarp();
         return true;
       };
-      auto issue_s = [&](int i) -> bool {
-        if (!mbar_wait_warp(&k_full[i & 1], (i >> 1) & 1, abort_flag)) return false;
-        tc_fence_after();
+      auto issue_s = [&](int i) {
         const uint64_t kd = kd0 + (uint64_t)(i & 1) * kTileStep;
         if (elect_one()) {
 #pragma unroll
@@ -340,21 +337,35 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           umma_commit(&k_empty[i & 1]);
         }
         __syncwarp();
-        return true;
       };
-      if (i0 < iend) {
+      // block b: PV of the chain's tile b - 1, S of its tile b.  The chains
+      // take turns block by block: left to themselves they fall into step,
+      // both in their softmax and then both on the tensor pipe.
+      const int n = max(0, (iend - i0 + step - 1) / step);
+      const int n_other = t == 1 ? max(0, ((one ? nj : end0 - j0) + step - 1) / step) : max(0, one ? nj / 2 : nj);
+      if (n > 0) {
         ok = mbar_wait_warp(&q_full[one ? 0 : t], 0, abort_flag);
         fence_proxy_async_smem();
-        int prev = -1, ph = 0;
-        for (int i = i0; i < iend && ok; i += step) {
-          if (prev >= 0) {
-            ok = issue_pv(prev, ph++);
-            if (!ok) break;
-          }
-          ok = issue_s(i);
-          prev = i;
+      }
+      for (int b = 0; b <= n && ok && n > 0; ++b) {
+        const int i = i0 + b * step, prev = i - step;
+        if (b < n) ok = mbar_wait_warp(&k_full[i & 1], (i >> 1) & 1, abort_flag);
+        if (ok && b > 0)
+          ok = mbar_wait_warp(&v_full[prev & 1], (prev >> 1) & 1, abort_flag) &&
+               (j0 + prev != cut || mbar_wait_warp(v_fixed, 0, abort_flag));
+        if (ok && b < n) {
+          const int pass = t == 0 ? b - 1 : b;  // the other chain's block that comes first
+          if (pass >= 0 && pass < n_other) ok = mbar_wait_warp(&turn[t], pass & 1, abort_flag);
         }
-        if (ok) ok = issue_pv(prev, ph);
+        // last, so that the waits above are over by the time P is there
+        if (ok && b > 0) ok = mbar_wait_warp(&p_head[t], (b - 1) & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        if (b > 0) ok = issue_pv(prev, b - 1);
+        if (ok && b < n) {
+          issue_s(i);
+          if (lane == 0) mbar_arrive(&turn[t ^ 1]);
+        }
       }
       if (elect_one()) {
         if (ok) umma_commit(&o_done[t]);
@@ -660,6 +671,8 @@ constexpr int kSms = 148;
 
 // Row tile pairs of packed sequences (an upper bound, see find_pair).
 static long long row_pairs(int Tq, int G, int nseq) { return ((long long)Tq * G >> 8) + nseq; }
+// and of one sequence of known length.
+static long long row_pairs_one(int n, int G) { return ((long long)n * G + 255) >> 8; }
 
 // CTAs per row tile pair: where the pairs leave SMs idle, the keys are split
 // so that about every SM has a CTA, in parts of at least 4 key tiles.

@@ -24,11 +24,12 @@ namespace {
 constexpr int kRowsThreads = 160;  // 4 warps of 16 keys, 1 loader
 constexpr int kRowsKeys = 64;      // keys per tile
 constexpr int kFinishKeys = 1024;  // keys per CTA of the weights' part
+constexpr int kFinishHeads = 4;    // heads whose scores are loaded ahead
 
 template <int D>
 struct RowsSmem {
   static constexpr int kTileBytes = kRowsKeys * D * 2;
-  static constexpr int kStages = D == 128 ? 3 : 6;  // 96 KB in flight, two CTAs per SM
+  static constexpr int kStages = D == 128 ? 2 : 4;  // 64 KB in flight, three CTAs per SM
   static constexpr int kRing = 0;                   // [stage][K, V]
   static constexpr int kMl = kRing + kStages * 2 * kTileBytes;  // [4 warps][16 rows] maxima, then sums
   static constexpr int kBars = kMl + 2 * 4 * 16 * 4;
@@ -84,7 +85,7 @@ struct RowsArgs {
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kRowsThreads, 2)
+__global__ void __launch_bounds__(kRowsThreads, 3)
     rows_kernel(RowsArgs a, const __grid_constant__ CUtensorMap tmap_kp, const __grid_constant__ CUtensorMap tmap_vp,
                 const __grid_constant__ CUtensorMap tmap_kc, const __grid_constant__ CUtensorMap tmap_vc) {
   using L = RowsSmem<D>;
@@ -332,7 +333,20 @@ __global__ void __launch_bounds__(256) finish_kernel(RowsArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const size_t rows = (size_t)a.B * a.Hq, row0 = (size_t)b * a.Hq + hk * a.G;
   const int n = a.weights ? live_slots(a.lens, b, a.cap) : 0;
+  const int j0 = blockIdx.y * kFinishKeys + threadIdx.x;
   if (blockIdx.y > 0 && (int)blockIdx.y * kFinishKeys >= n) return;
+  // the first heads' scores and the weights are on their way while lse forms
+  const float* score = a.score + (size_t)bh * a.G * a.cap;
+  float* weights = a.weights + (size_t)bh * a.cap;
+  float x[kFinishHeads][kFinishKeys / 256], w[kFinishKeys / 256];
+#pragma unroll
+  for (int e = 0; e < kFinishKeys / 256; ++e) {
+    const int j = j0 + 256 * e;
+    w[e] = j < n ? weights[j] : 0.f;
+#pragma unroll
+    for (int g = 0; g < kFinishHeads; ++g) x[g][e] = j < n && g < a.G ? score[(size_t)g * a.cap + j] : -INFINITY;
+  }
+#pragma unroll 1
   for (int g = warp; g < a.G; g += 8) {
     float top = -INFINITY, sum = 0.f;
     for (int i = lane; i < a.nslot; i += 32) top = fmaxf(top, a.lse_part[i * rows + row0 + g]);
@@ -363,13 +377,17 @@ __global__ void __launch_bounds__(256) finish_kernel(RowsArgs a) {
   }
   if (!a.weights) return;
   __syncthreads();
-  const int j1 = min(n, (int)(blockIdx.y + 1) * kFinishKeys);
-  const float* score = a.score + (size_t)bh * a.G * a.cap;
-  float* w = a.weights + (size_t)bh * a.cap;
-  for (int j = blockIdx.y * kFinishKeys + threadIdx.x; j < j1; j += 256) {
+#pragma unroll
+  for (int e = 0; e < kFinishKeys / 256; ++e) {
+    const int j = j0 + 256 * e;
+    if (j >= n) break;
     float sum = 0.f;
-    for (int g = 0; g < a.G; ++g) sum += ex2_approx(score[(size_t)g * a.cap + j] - lse2[g]);
-    w[j] += sum;
+#pragma unroll
+    for (int g = 0; g < kFinishHeads; ++g)
+      if (g < a.G) sum += ex2_approx(x[g][e] - lse2[g]);
+#pragma unroll 1
+    for (int g = kFinishHeads; g < a.G; ++g) sum += ex2_approx(score[(size_t)g * a.cap + j] - lse2[g]);
+    weights[j] = w[e] + sum;
   }
 }
 
@@ -383,10 +401,11 @@ struct StepPlan {
 StepPlan step_plan(const StepArgs& a, bool with_weights) {
   StepPlan p{};
   const int own_rows = (a.G + 15) / 16;
-  // own: enough CTAs for a few waves of two per SM, at least 8 tiles each
+  // own: enough CTAs for a few waves of three per SM, at least 16 tiles of a
+  // full cache each
   const long long ctas = (long long)a.B * a.Hkv * own_rows;
   long long n = (8 * kSms + ctas - 1) / ctas;
-  if (n > a.cap / 512) n = a.cap / 512;
+  if (n > a.cap / 1024) n = a.cap / 1024;
   if (n > 64) n = 64;
   p.nown = a.cap == 0 ? 0 : n < 1 ? 1 : (int)n;
   if (a.P > 0) {
@@ -396,7 +415,7 @@ StepPlan step_plan(const StepArgs& a, bool with_weights) {
       if (n > 64) n = 64;
       p.npre_rows = n < 1 ? 1 : (int)n;
     } else {
-      p.npre_tc = key_splits(row_pairs(a.B, a.G, 1) * a.Hkv, a.P);
+      p.npre_tc = key_splits(row_pairs_one(a.B, a.G) * a.Hkv, a.P);
     }
   }
   const int nslot = p.nown + p.npre_rows + p.npre_tc;
@@ -449,7 +468,7 @@ cudaError_t run_step(const StepArgs& s, const StepPlan& p, cudaStream_t st) {
     t.Tq = s.B;
     t.Tk = s.P;
     t.nsplit = p.npre_tc;
-    t.ntile = (int)row_pairs(s.B, s.G, 1);
+    t.ntile = (int)row_pairs_one(s.B, s.G);
     t.partial = true;
     t.scale_log2 = s.scale_log2;
     t.q_tok = s.q_seq;
