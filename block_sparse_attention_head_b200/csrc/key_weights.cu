@@ -83,19 +83,16 @@ __global__ void __launch_bounds__(kKwThreads, 1)
   const int t_glob = blockIdx.x / a.Hkv / a.nsplit;
 
   if (warp == 0) {
-    int lp = 0;
-    const int s = find_pair(a.cu_k, a.nseq, 1, t_glob, lp);
-    if (lane == 0) {
-      work[0] = s;
-      work[1] = lp;
-    }
+    const SeqPair p = find_pair(a.cu_k, a.cu_q, a.nseq, 1, t_glob);
+    if (lane == 0) *reinterpret_cast<SeqPair*>(work) = p;
   }
   __syncthreads();
-  const int s = work[0], local = work[1];
-  if (s < 0 || local < 0) return;
-  int q0s, q1s, k0s, k1s;
-  seq_rows(a.cu_q, s, a.Tq, q0s, q1s);
-  seq_rows(a.cu_k, s, a.Tk, k0s, k1s);
+  const SeqPair sp = *reinterpret_cast<const SeqPair*>(work);
+  const int local = sp.local;
+  if (sp.seq < 0 || local < 0) return;
+  int q0s = sp.other_lo, q1s = sp.other_hi, k0s = sp.lo, k1s = sp.hi;
+  clamp_rows(q0s, q1s, a.Tq);
+  clamp_rows(k0s, k1s, a.Tk);
   const int nq = q1s - q0s, nk = k1s - k0s;
   const int kb = local * kKwTile;  // first key of the pair
   if (kb >= nk) return;

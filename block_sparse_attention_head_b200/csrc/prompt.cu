@@ -142,23 +142,41 @@ struct TcArgs {
 // f(s) = floor(cu_q[s] G / 256) + s: at least ceil(n_q G / 256) of them (the
 // others are idle), and f needs no sum over the sequences before, so a warp
 // finds s by a 32-way search.
-__device__ __forceinline__ int first_pair(const int32_t* cu, int s, int G) {
-  return (int)(((long long)cu[s] * G) >> 8) + s;
-}
-__device__ __forceinline__ int find_pair(const int32_t* cu, int nseq, int G, int t, int& local) {
+// The sequence of pair number t (-1: none), t's place in it and its rows; the
+// ends are loaded along with the keys of the search, in one round for up to 32
+// sequences.
+struct SeqPair {
+  int seq, local, lo, hi, other_lo, other_hi;
+};
+__device__ __forceinline__ SeqPair find_pair(const int32_t* cu, const int32_t* cu_other, int nseq, int G, int t) {
   const int lane = threadIdx.x & 31;
+  SeqPair p{-1, 0, 0, 0, 0, 0};
   int lo = 0, hi = nseq;
   bool found = false;
   while (hi - lo > 1 || !found) {
     const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-    const unsigned hit = __ballot_sync(0xffffffffu, at < hi && first_pair(cu, at, G) <= t);
-    if (!hit) return -1;
-    lo += (31 - __clz(hit)) * step;
+    int c0 = 0, c1 = 0, o0 = 0, o1 = 0;
+    if (at < hi) {
+      c0 = cu[at];
+      c1 = cu[at + 1];
+      o0 = cu_other[at];
+      o1 = cu_other[at + 1];
+    }
+    const int first = (int)(((long long)c0 * G) >> 8) + at;
+    const unsigned hit = __ballot_sync(0xffffffffu, at < hi && first <= t);
+    if (!hit) return p;
+    const int src = 31 - __clz(hit);
+    p.local = t - __shfl_sync(0xffffffffu, first, src);
+    p.lo = __shfl_sync(0xffffffffu, c0, src);
+    p.hi = __shfl_sync(0xffffffffu, c1, src);
+    p.other_lo = __shfl_sync(0xffffffffu, o0, src);
+    p.other_hi = __shfl_sync(0xffffffffu, o1, src);
+    lo += src * step;
     hi = min(hi, lo + step);
     found = true;
   }
-  local = t - first_pair(cu, lo, G);
-  return lo;
+  p.seq = lo;
+  return p;
 }
 
 template <typename T, int D>
@@ -188,6 +206,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   int* work = misc + 2;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 320) {
+    prefetch_tmap(&tmap_k);
+    prefetch_tmap(&tmap_v);
+  }
   const int hk = blockIdx.x % a.Hkv;
   const int t_glob = (blockIdx.x / a.Hkv) % a.ntile;
   const int z = blockIdx.x / a.Hkv / a.ntile;
@@ -196,19 +218,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   int q0s = 0, q1s = a.Tq, k0s = 0, k1s = a.Tk, local = t_glob;
   if (a.cu_q) {
     if (warp == 0) {
-      int lp = 0;
-      const int s = find_pair(a.cu_q, a.nseq, a.G, t_glob, lp);
-      if (lane == 0) {
-        work[0] = s;
-        work[1] = lp;
-      }
+      const SeqPair p = find_pair(a.cu_q, a.cu_k, a.nseq, a.G, t_glob);
+      if (lane == 0) *reinterpret_cast<SeqPair*>(work) = p;
     }
     __syncthreads();
-    const int s = work[0];
-    if (s < 0) return;
-    local = work[1];
-    seq_rows(a.cu_q, s, a.Tq, q0s, q1s);
-    seq_rows(a.cu_k, s, a.Tk, k0s, k1s);
+    const SeqPair p = *reinterpret_cast<const SeqPair*>(work);
+    if (p.seq < 0) return;
+    local = p.local;
+    q0s = p.lo;
+    q1s = p.hi;
+    k0s = p.other_lo;
+    k1s = p.other_hi;
+    clamp_rows(q0s, q1s, a.Tq);
+    clamp_rows(k0s, k1s, a.Tk);
   }
   const int nq = q1s - q0s, nk = k1s - k0s, G = a.G;
   const int R = nq * G;
@@ -394,26 +416,41 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int rt = r0 + 128 * t;   // first row of the tile
     const uint32_t lane_off = (uint32_t)((32 * qd) << 16);
     const uint32_t s_col = tmem + lane_off + 128 * t, o_col = tmem + lane_off + kTcO + 128 * t;
-    // this warp's 32 query rows, whole rows at a time
-    {
-      const int rr = rt + r;
-      const int64_t off = r < nrows ? (q0s + rr / G) * a.q_tok + (hk * G + rr % G) * a.q_head : -1;
-      const T* Q = static_cast<const T*>(a.Q);
-      const int ch = lane % kChunks;
-      if (nrows > 0) {
+    // this warp's 32 query rows, whole rows at a time: lane -> row lane /
+    // kChunks of a step, 16-byte chunk lane % kChunks
+    const int ch = lane % kChunks;
+    if (nrows > 0) {
+      int row = 32 * qd + lane / kChunks;
+      const int tok0 = rt / G, tok1 = (rt + row) / G;
+      int head = rt + row - tok1 * G;
+      const T* Q = static_cast<const T*>(a.Q) + (int64_t)q0s * a.q_tok + (int64_t)(hk * G) * a.q_head + 8 * ch;
+      const T* first = Q + (int64_t)tok0 * a.q_tok + (int64_t)(rt - tok0 * G) * a.q_head;  // a row that exists
+      const T* at = Q + (int64_t)tok1 * a.q_tok + (int64_t)head * a.q_head;
+      const int64_t wrap = a.q_tok - (int64_t)G * a.q_head;
+      uint4 v[32 / kRowsPerStep];  // every load on its way before the first is stored
 #pragma unroll
-        for (int i = 0; i < 32 / kRowsPerStep; ++i) {
-          const int from = i * kRowsPerStep + lane / kChunks;
-          const int64_t o = __shfl_sync(0xffffffffu, off, from);
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (o >= 0) v = __ldg(reinterpret_cast<const uint4*>(Q + o) + ch);
-          st_shared_v4(q_s + t * L::kTileBytes + (ch >> 3) * 16384 + sw128_offset(32 * qd + from, ch & 7), v.x, v.y,
-                       v.z, v.w);
+      for (int i = 0; i < 32 / kRowsPerStep; ++i) {
+        v[i] = __ldg(reinterpret_cast<const uint4*>(row < nrows ? at : first));
+        row += kRowsPerStep;
+        head += kRowsPerStep;
+        at += kRowsPerStep * a.q_head;
+#pragma unroll
+        for (int e = 0; e < kRowsPerStep; ++e) {  // at most one token further per row
+          const bool over = head >= G;
+          head -= over ? G : 0;
+          at += over ? wrap : 0;
         }
       }
-      fence_proxy_async_smem();
-      mbar_arrive(&q_full[t]);
+      row = 32 * qd + lane / kChunks;
+#pragma unroll
+      for (int i = 0; i < 32 / kRowsPerStep; ++i, row += kRowsPerStep) {
+        const bool there = row < nrows;
+        st_shared_v4(q_s + t * L::kTileBytes + (ch >> 3) * 16384 + sw128_offset(row, ch & 7), there ? v[i].x : 0u,
+                     there ? v[i].y : 0u, there ? v[i].z : 0u, there ? v[i].w : 0u);
+      }
     }
+    fence_proxy_async_smem();
+    mbar_arrive(&q_full[t]);
     const int see = one || t == 0 ? (r < rows0 ? seen(r0 + r) : 0) : (r < rows1 ? seen(rt + r) : 0);
     // tiles below `whole` need no mask in any row of the tile
     const int whole = (one ? seen(r0) : seen(min(rt, R - 1))) >> 7;
@@ -546,54 +583,75 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         else if (a.lse)
           a.lse[(size_t)head * a.Tq + tok] = lse2 * kLn2;
       }
-      if (!a.partial || have) {
+      if (!a.partial || have) {  // an empty part's rows are not read
+        // 128 bytes of every row at a time through this warp's rows of the
+        // query tile (no MMA reads it any more), so that a store writes whole
+        // lines: 32 fp32 columns of a part, 64 of O
+        uint8_t* stage = smem + L::kQ + t * L::kTileBytes + 32 * qd * 128;
+        const uint32_t stage_s = smem_u32(stage);
+        const int64_t off = !valid      ? -1
+                            : a.partial ? (int64_t)((((size_t)z * a.Tq + tok) * a.Hq + head) * D * 4)
+                                        : (tok * a.o_tok + head * a.o_head) * 2;
+        uint8_t* out = a.partial ? reinterpret_cast<uint8_t*>(a.o_part) : static_cast<uint8_t*>(a.O);
+        const bool zero = !have || __any_sync(0xffffffffu, l == 0.f);
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          float o[32];
+        for (int c = 0; c < D / 64; ++c) {
+          float o[2][32];
           if (have) {
-            tmem_ld32(o_col + 32 * c, o);
+            tmem_ld32(o_col + 64 * c, o[0]);
+            tmem_ld32(o_col + 64 * c + 32, o[1]);
             tmem_wait_ld();
-            pin_regs32(o);
+            pin_regs32(o[0]);
+            pin_regs32(o[1]);
             if (have1) {
-              float o1[32];
-              tmem_ld32(o_col + 128 + 32 * c, o1);
-              tmem_wait_ld();
-              pin_regs32(o1);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = o[e] * w0 + o1[e] * w1;
+              for (int h = 0; h < 2; ++h) {
+                float o1[32];
+                tmem_ld32(o_col + 128 + 64 * c + 32 * h, o1);
+                tmem_wait_ld();
+                pin_regs32(o1);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[h][e] = o[h][e] * w0 + o1[e] * w1;
+              }
             }
           }
+          if (zero) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = have && l != 0.f ? o[e] * inv : 0.f;
+            for (int e = 0; e < 64; ++e) o[e >> 5][e & 31] = have && l != 0.f ? o[e >> 5][e & 31] : 0.f;
+          }
+#pragma unroll
+          for (int e = 0; e < 64; ++e) o[e >> 5][e & 31] *= inv;
+          auto copy_out = [&](int col) {  // col: bytes from the row's start
+            __syncwarp();
+            uint4 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              v[i] = *reinterpret_cast<const uint4*>(stage + sw128_offset(4 * i + lane / 8, lane & 7));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int64_t to = __shfl_sync(0xffffffffu, off, 4 * i + lane / 8);
+              if (to >= 0) *reinterpret_cast<uint4*>(out + to + col + 16 * (lane & 7)) = v[i];
+            }
+            __syncwarp();
+          };
           if (a.partial) {
-            if (valid) {
-              float4* dst =
-                  reinterpret_cast<float4*>(a.o_part + (((size_t)z * a.Tq + tok) * a.Hq + head) * D + 32 * c);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                st_shared_v4(stage_s + sw128_offset(lane, e), __float_as_uint(o[h][4 * e]),
+                             __float_as_uint(o[h][4 * e + 1]), __float_as_uint(o[h][4 * e + 2]),
+                             __float_as_uint(o[h][4 * e + 3]));
+              copy_out(256 * c + 128 * h);
             }
           } else {
-            // staged in the row tile's shared memory (no MMA reads Q any more)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              st_shared_v4(q_s + t * L::kTileBytes + (c >> 1) * 16384 + sw128_offset(r, (4 * c + e) & 7),
-                           pack16<T>(o[8 * e], o[8 * e + 1]), pack16<T>(o[8 * e + 2], o[8 * e + 3]),
-                           pack16<T>(o[8 * e + 4], o[8 * e + 5]), pack16<T>(o[8 * e + 6], o[8 * e + 7]));
-          }
-        }
-        if (!a.partial) {
-          __syncwarp();
-          const int64_t off = valid ? tok * a.o_tok + head * a.o_head : -1;
-          T* O = static_cast<T*>(a.O);
-          const int ch = lane % kChunks;
-#pragma unroll
-          for (int i = 0; i < 32 / kRowsPerStep; ++i) {
-            const int from = i * kRowsPerStep + lane / kChunks;
-            const int64_t o = __shfl_sync(0xffffffffu, off, from);
-            const uint4 v = *reinterpret_cast<const uint4*>(smem + L::kQ + t * L::kTileBytes + (ch >> 3) * 16384 +
-                                                            sw128_offset(32 * qd + from, ch & 7));
-            if (o >= 0) reinterpret_cast<uint4*>(O + o)[ch] = v;
+            for (int e = 0; e < 8; ++e)
+              st_shared_v4(stage_s + sw128_offset(lane, e), pack16<T>(o[e >> 2][8 * (e & 3)], o[e >> 2][8 * (e & 3) + 1]),
+                           pack16<T>(o[e >> 2][8 * (e & 3) + 2], o[e >> 2][8 * (e & 3) + 3]),
+                           pack16<T>(o[e >> 2][8 * (e & 3) + 4], o[e >> 2][8 * (e & 3) + 5]),
+                           pack16<T>(o[e >> 2][8 * (e & 3) + 6], o[e >> 2][8 * (e & 3) + 7]));
+            copy_out(128 * c);
           }
         }
       }

@@ -92,10 +92,8 @@ __device__ __forceinline__ __half from_f32<__half>(float x) {
   return __float2half_rn(x);
 }
 
-// Rows [lo, hi) of packed sequence s, clamped into [0, T].
-__device__ __forceinline__ void seq_rows(const int32_t* cu, int s, int T, int& lo, int& hi) {
-  lo = cu[s];
-  hi = cu[s + 1];
+// Rows [lo, hi) of a packed sequence, clamped into [0, T].
+__device__ __forceinline__ void clamp_rows(int& lo, int& hi, int T) {
   if (lo < 0 || hi < lo || hi > T) {
     raise_error(kErrIndex);
     lo = min(max(lo, 0), T);
