@@ -206,6 +206,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   int* work = misc + 2;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  launch_dependents();
   if (tid == 320) {
     prefetch_tmap(&tmap_k);
     prefetch_tmap(&tmap_v);

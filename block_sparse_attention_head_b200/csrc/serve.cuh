@@ -70,6 +70,24 @@ struct EvictArgs {
 size_t evict_ws(int B, int Hkv, int budget);
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
 
+// Launches kernel(args...); overlap: it may start before the kernel in front of
+// it in the stream has ended (see launch_dependents).
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, bool overlap, cudaStream_t s,
+                         const A&... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = overlap ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ------------------------------------------------------------ device helpers
 template <typename T>
 __device__ __forceinline__ float to_f32(T x);
@@ -110,6 +128,13 @@ __device__ __forceinline__ int live_slots(const int32_t* lens, int b, int cap) {
   }
   return n;
 }
+
+// Overlapped launches (programmatic dependent launch).  A kernel launched with
+// launch_after may start once every CTA of the kernel before it has called
+// launch_dependents or ended; wait_prior_grids returns when that kernel is
+// complete and its writes are visible (at once after an ordinary launch).
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_prior_grids() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll

@@ -16,6 +16,9 @@
 //           the same launch.
 //   finish  join, and add the own keys' weights 2^(score - lse) from the scores
 //           that rows_kernel left (4 G bytes per key beside the 4 d it read).
+// The launches overlap: rows_kernel may start while attend_kernel's last CTAs
+// run (neither reads what the other writes), finish_kernel's CTAs wait where
+// they need the parts.
 #include "serve.cuh"
 
 namespace ig {
@@ -23,13 +26,16 @@ namespace ig {
 namespace {
 constexpr int kRowsThreads = 160;  // 4 warps of 16 keys, 1 loader
 constexpr int kRowsKeys = 64;      // keys per tile
-constexpr int kFinishKeys = 1024;  // keys per CTA of the weights' part
-constexpr int kFinishHeads = 4;    // heads whose scores are loaded ahead
+constexpr int kFinishKeys = 4096;  // keys per CTA of the weights' part
 
-template <int D>
+// kLong: 96 KB in flight and two CTAs per SM, the faster stream; else 64 KB and
+// three CTAs, whose starts and ends hide one another, for short shares.
+// Measured, d = 128: 8 caches of 65000 keys 228 us against 248, 128 caches of
+// 200 keys 33 us against 28.
+template <int D, bool kLong>
 struct RowsSmem {
   static constexpr int kTileBytes = kRowsKeys * D * 2;
-  static constexpr int kStages = D == 128 ? 2 : 4;  // 64 KB in flight, three CTAs per SM
+  static constexpr int kStages = (D == 128 ? 1 : 2) * (kLong ? 3 : 2);
   static constexpr int kRing = 0;                   // [stage][K, V]
   static constexpr int kMl = kRing + kStages * 2 * kTileBytes;  // [4 warps][16 rows] maxima, then sums
   static constexpr int kBars = kMl + 2 * 4 * 16 * 4;
@@ -84,11 +90,11 @@ struct RowsArgs {
   float* weights;
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kRowsThreads, 3)
+template <typename T, int D, bool kLong>
+__global__ void __launch_bounds__(kRowsThreads, kLong ? 2 : 3)
     rows_kernel(RowsArgs a, const __grid_constant__ CUtensorMap tmap_kp, const __grid_constant__ CUtensorMap tmap_vp,
                 const __grid_constant__ CUtensorMap tmap_kc, const __grid_constant__ CUtensorMap tmap_vc) {
-  using L = RowsSmem<D>;
+  using L = RowsSmem<D, kLong>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* ml = reinterpret_cast<float*>(smem + L::kMl);
@@ -97,6 +103,7 @@ __global__ void __launch_bounds__(kRowsThreads, 3)
   volatile int* abort_flag = reinterpret_cast<int*>(smem + L::kMisc);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+  launch_dependents();
   // ---- which rows, which keys
   int idx = blockIdx.x, hk, b0, rows, row0, n, split, nsplit, slot, z;
   const bool pre = idx < a.npre * a.Hkv;
@@ -290,6 +297,7 @@ __global__ void __launch_bounds__(kRowsThreads, 3)
         *reinterpret_cast<float2*>(ow + (warp * 16 + (lane >> 2) + 8 * h) * D + 8 * d + (lane & 3) * 2) =
             make_float2(o[d][2 * h] * w[h], o[d][2 * h + 1] * w[h]);
   }
+  wait_prior_grids();  // this grid's end is the prefix's, too
   named_bar_sync(1, 128);
   if (*abort_flag) return;
   for (int x = tid; x < 16 * (D / 4); x += 128) {
@@ -324,29 +332,19 @@ __global__ void __launch_bounds__(kRowsThreads, 3)
   }
 }
 
-// Joins the parts of the G rows of one (sequence, key/value head) and adds the
-// weights of kFinishKeys of its own keys.
+// blockIdx.y = 0 joins the parts of the G rows of one (sequence, key/value
+// head); the others add the weights of kFinishKeys of its own keys each.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) finish_kernel(RowsArgs a) {
   extern __shared__ float lse2[];  // [G]
   const int bh = blockIdx.x, b = bh / a.Hkv, hk = bh % a.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const size_t rows = (size_t)a.B * a.Hq, row0 = (size_t)b * a.Hq + hk * a.G;
-  const int n = a.weights ? live_slots(a.lens, b, a.cap) : 0;
-  const int j0 = blockIdx.y * kFinishKeys + threadIdx.x;
-  if (blockIdx.y > 0 && (int)blockIdx.y * kFinishKeys >= n) return;
-  // the first heads' scores and the weights are on their way while lse forms
-  const float* score = a.score + (size_t)bh * a.G * a.cap;
-  float* weights = a.weights + (size_t)bh * a.cap;
-  float x[kFinishHeads][kFinishKeys / 256], w[kFinishKeys / 256];
-#pragma unroll
-  for (int e = 0; e < kFinishKeys / 256; ++e) {
-    const int j = j0 + 256 * e;
-    w[e] = j < n ? weights[j] : 0.f;
-#pragma unroll
-    for (int g = 0; g < kFinishHeads; ++g) x[g][e] = j < n && g < a.G ? score[(size_t)g * a.cap + j] : -INFINITY;
-  }
-#pragma unroll 1
+  const bool join = blockIdx.y == 0;
+  const int n = join ? 0 : live_slots(a.lens, b, a.cap);
+  const int j0 = ((int)blockIdx.y - 1) * kFinishKeys;
+  if (!join && j0 >= n) return;
+  wait_prior_grids();
   for (int g = warp; g < a.G; g += 8) {
     float top = -INFINITY, sum = 0.f;
     for (int i = lane; i < a.nslot; i += 32) top = fmaxf(top, a.lse_part[i * rows + row0 + g]);
@@ -357,37 +355,51 @@ __global__ void __launch_bounds__(256) finish_kernel(RowsArgs a) {
     sum = warp_sum(sum);
     const float y = sum == 0.f ? -INFINITY : top + log2f(sum);
     if (lane == 0) lse2[g] = y;
-    if (blockIdx.y > 0) continue;
+    if (!join) continue;
     if (lane == 0 && a.lse) a.lse[row0 + g] = y * kLn2;
     float o[D / 32];
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
+    for (int i0 = 0; i0 < a.nslot; i0 += 32) {
+      // lane i: the weight of part i0 + i (an empty part's rows were not written)
+      const float x = i0 + lane < a.nslot ? a.lse_part[(i0 + lane) * rows + row0 + g] : -INFINITY;
+      const float w = x == -INFINITY ? 0.f : exp2f(x - y);
+      const unsigned some = __ballot_sync(0xffffffffu, x != -INFINITY);
+      const int end = min(32, a.nslot - i0);
 #pragma unroll 4
-    for (int i = 0; i < a.nslot; ++i) {
-      const float x = a.lse_part[i * rows + row0 + g];
-      if (x == -INFINITY) continue;  // an empty part's rows were not written
-      const float w = exp2f(x - y);
-      const float* src = a.o_part + (i * rows + row0 + g) * D;
+      for (int i = 0; i < end; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, w, i);
+        const float* src = a.o_part + ((i0 + i) * rows + row0 + g) * D + lane * (D / 32);
+        float v[D / 32];
+        if constexpr (D == 128)
+          *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
+        else
+          *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) o[e] = fmaf(w, src[lane + 32 * e], o[e]);
+        for (int e = 0; e < D / 32; ++e) o[e] = (some >> i) & 1 ? fmaf(wi, v[e], o[e]) : o[e];
+      }
     }
-    T* dst = static_cast<T*>(a.O) + (row0 + g) * D;
+    T* dst = static_cast<T*>(a.O) + (row0 + g) * D + lane * (D / 32);
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) dst[lane + 32 * e] = from_f32<T>(o[e]);
+    for (int e = 0; e < D / 32; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack16<T>(o[e], o[e + 1]);
   }
-  if (!a.weights) return;
+  if (join) return;
   __syncthreads();
+  const float* score = a.score + (size_t)bh * a.G * a.cap;
+  float* weights = a.weights + (size_t)bh * a.cap;
+  const int j1 = min(n, j0 + kFinishKeys);
+  for (int j = j0 + threadIdx.x; j < j1; j += 4 * 256) {
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int g = 0; g < a.G; ++g) {
+      const float y = lse2[g];
 #pragma unroll
-  for (int e = 0; e < kFinishKeys / 256; ++e) {
-    const int j = j0 + 256 * e;
-    if (j >= n) break;
-    float sum = 0.f;
+      for (int e = 0; e < 4; ++e)
+        if (j + 256 * e < j1) sum[e] += ex2_approx(score[(size_t)g * a.cap + j + 256 * e] - y);
+    }
 #pragma unroll
-    for (int g = 0; g < kFinishHeads; ++g)
-      if (g < a.G) sum += ex2_approx(x[g][e] - lse2[g]);
-#pragma unroll 1
-    for (int g = kFinishHeads; g < a.G; ++g) sum += ex2_approx(score[(size_t)g * a.cap + j] - lse2[g]);
-    weights[j] = w[e] + sum;
+    for (int e = 0; e < 4; ++e)
+      if (j + 256 * e < j1) weights[j + 256 * e] += sum[e];
   }
 }
 
@@ -427,6 +439,16 @@ StepPlan step_plan(const StepArgs& a, bool with_weights) {
   p.total = p.score + (with_weights ? up(rows * a.cap * 4) : 0);
   if (p.total < 256) p.total = 256;
   return p;
+}
+
+template <typename T, int D, bool kLong>
+cudaError_t run_rows(const RowsArgs& a, unsigned ctas, bool after_prefix, const CUtensorMap& kp, const CUtensorMap& vp,
+                     const CUtensorMap& kc, const CUtensorMap& vc, cudaStream_t st) {
+  const size_t sm = RowsSmem<D, kLong>::bytes();
+  const cudaError_t e =
+      cudaFuncSetAttribute(rows_kernel<T, D, kLong>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+  if (e != cudaSuccess) return e;
+  return launch_after(rows_kernel<T, D, kLong>, dim3(ctas), kRowsThreads, sm, after_prefix, st, a, kp, vp, kc, vc);
 }
 
 template <typename T, int D>
@@ -495,17 +517,15 @@ cudaError_t run_step(const StepArgs& s, const StepPlan& p, cudaStream_t st) {
       e = make_tmap_rows(&vc, own ? s.Vc : s.Q, s.dtype, D, own ? s.cap : 1, s.B * s.Hkv, D,
                          own ? (int64_t)s.cap * D : D, kRowsKeys);
     if (e != cudaSuccess) return e;
-    const size_t sm = RowsSmem<D>::bytes();
-    e = cudaFuncSetAttribute(rows_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
-    if (e != cudaSuccess) return e;
-    rows_kernel<T, D><<<(unsigned)ctas, kRowsThreads, sm, st>>>(a, kp, vp, kc, vc);
-    e = cudaGetLastError();
+    // by the longest share: 16 tiles and more stream
+    const int share = max(a.nown ? s.cap / a.nown : 0, a.npre ? s.P / a.npre : 0);
+    e = share >= 16 * kRowsKeys ? run_rows<T, D, true>(a, (unsigned)ctas, p.npre_tc > 0, kp, vp, kc, vc, st)
+                                : run_rows<T, D, false>(a, (unsigned)ctas, p.npre_tc > 0, kp, vp, kc, vc, st);
     if (e != cudaSuccess) return e;
   }
   if (p.direct && ctas > 0) return cudaSuccess;
-  const dim3 grid(s.B * s.Hkv, s.weights ? (unsigned)max(1, (s.cap + kFinishKeys - 1) / kFinishKeys) : 1u);
-  finish_kernel<T, D><<<grid, 256, s.G * 4, st>>>(a);
-  return cudaGetLastError();
+  const dim3 grid(s.B * s.Hkv, 1u + (s.weights ? (unsigned)((s.cap + kFinishKeys - 1) / kFinishKeys) : 0u));
+  return launch_after(finish_kernel<T, D>, grid, 256, s.G * 4, ctas > 0, st, a);
 }
 }  // namespace
 
