@@ -108,7 +108,7 @@ def lib():
         "instagen_pq_votes": (ctypes.c_int, [PP, PP, PP, PP, PP, PP, P, PP, PP, sz, vp]),
         "instagen_select_sample_votes": (ctypes.c_int, [PP, PP, PP, PP, P, PP, PP, PP, PP, vp]),
     }
-    PR, PC = ctypes.POINTER(PromptParams), ctypes.POINTER(CacheParams)
+    PR = PC = ctypes.c_void_p  # instagen_prompt_params, instagen_cache_params: a struct's address or its bytes
     sig.update({
         "instagen_prompt_attention_workspace_size": (sz, [PR]),
         "instagen_prompt_attention": (ctypes.c_int, [PP, PP, PP, PP, PP, PR, PP, PP, PP, sz, vp]),

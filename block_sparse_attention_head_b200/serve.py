@@ -1,25 +1,36 @@
 """Binding of the language-model entry points of ``libinstagen.so``:
 ``prompt_attention``, ``key_weights``, ``prefix_attention`` and ``evict``
-(argument marshalling only; the contracts are in ``include/instagen.h``)."""
+(argument marshalling only; the contracts are in ``include/instagen.h``).
+
+A call for a few short sequences runs for some microseconds on the GPU, so the
+marshalling is kept short: every check is made once, a tensor that fails one is
+handed to a slower function that says why, and the parameter blocks are packed
+as the C structs lay them out (``PromptParams``, ``CacheParams``)."""
 from __future__ import annotations
 
-import ctypes
-import math
+import struct
 from typing import Optional
 
 import torch
 
-from . import CacheParams, InstaGenError, PromptParams, _check, _need, _ptr, _stream, lib
+from . import InstaGenError, _check, _need, lib
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}  # instagen_dtype
+_F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
+_prompt_block = struct.Struct("@8if4x8q").pack  # instagen_prompt_params
+_cache_block = struct.Struct("@7if2q").pack     # instagen_cache_params
 
 
-def _on_current(*tensors):
-    """Kernels run on the current device, so every tensor must live there."""
-    cur = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != cur:
-            raise InstaGenError(f"tensors must be on the current device cuda:{cur}, got {t.device}")
+def _device() -> int:
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else torch.cuda.current_device()
+
+
+def _stream(dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _wrong_device(t, dev):
+    raise InstaGenError(f"tensors must be on the current device cuda:{dev}, got {t.device}")
 
 
 def _dtype_of(t, name: str):
@@ -28,14 +39,25 @@ def _dtype_of(t, name: str):
     return t.dtype
 
 
-def _need_rows(t, name: str, dtype, shape):
-    """A 3-D tensor of rows: last dimension contiguous, the others strided in
-    whole 16-byte steps without overlap."""
+def _flat(t, name: str, dtype, shape, dev: int) -> int:
+    """Address of a contiguous tensor of this type and shape on device dev."""
+    if not (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous()):
+        _need(t, name, dtype, shape)
+        _wrong_device(t, dev)
+    return t.data_ptr()
+
+
+def _rows(t, name: str, dtype, shape, dev: int):
+    """Address and strides of a 3-D tensor of rows: last dimension contiguous,
+    the others strided in whole 16-byte steps without overlap."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise InstaGenError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-    if t.dtype != dtype:
+    if t.get_device() != dev:
+        if not t.is_cuda:
+            raise InstaGenError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+        _wrong_device(t, dev)
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
@@ -45,52 +67,50 @@ def _need_rows(t, name: str, dtype, shape):
         raise ValueError(f"{name}: the last dimension must be contiguous")
     if (n0 > 1 and (s0 < d or s0 % 8)) or (n1 > 1 and (s1 < d or s1 % 8)):
         raise ValueError(f"{name}: strides must be multiples of 8 elements and at least a row, got {t.stride()}")
+    return t.data_ptr(), s0, s1
 
 
 def _cache_shape(t, name: str, dtype):
-    _need(t, name, dtype)
-    if t.dim() != 4:
+    if not isinstance(t, torch.Tensor) or t.dim() != 4:
+        _need(t, name, dtype)
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [B, Hkv, slots, d]")
     return t.shape
 
 
-def _work_area(workspace: Optional[torch.Tensor], need: int, like: torch.Tensor, what: str):
+def _heads(Hq: int, Hkv: int):
+    if Hkv < 1 or Hq < 1 or Hq % Hkv:
+        raise ValueError(f"{Hq} query heads cannot share {Hkv} key/value heads")
+
+
+def _work_area(workspace: Optional[torch.Tensor], need: int, like: torch.Tensor, dev: int, what: str):
     if need == 0:
         raise InstaGenError(f"invalid or unsupported parameters for {what}")
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=like.device), need
+        workspace = like.new_empty((need,), dtype=_U8)
+        return workspace, workspace.data_ptr(), need
     have = workspace.numel() * workspace.element_size()
     if have < need:
         raise InstaGenError(f"workspace too small: {have} < {need}")
-    _on_current(workspace)
-    return workspace, have
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    if workspace.get_device() != dev:
+        _wrong_device(workspace, dev)
+    return workspace, workspace.data_ptr(), have
 
 
-def _prompt_params(q, k, v, o, cu_q, cu_k, causal, softmax_scale) -> PromptParams:
+def _prompt_shapes(q, k, cu_q, cu_k, dev: int):
     dt = _dtype_of(q, "q")
     if not isinstance(k, torch.Tensor):
         raise TypeError("k must be a torch.Tensor")
-    if q.dim() != 3 or k.dim() != 3 or k.shape[2] != q.shape[2]:
-        raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} must be [Tq, Hq, d] and [Tk, Hkv, d]")
-    Tq, Hq, d = q.shape
-    Tk, Hkv = k.shape[:2]
-    _need_rows(q, "q", dt, q.shape)
-    _need_rows(k, "k", dt, k.shape)
-    if Hkv < 1 or Hq < 1 or Hq % Hkv:
-        raise ValueError(f"{Hq} query heads cannot share {Hkv} key/value heads")
-    if v is not None:
-        _need_rows(v, "v", dt, k.shape)
-    if o is not None:
-        _need_rows(o, "out", dt, q.shape)
-    _need(cu_q, "cu_q", torch.int32)
-    _need(cu_k, "cu_k", torch.int32, cu_q.shape)
-    if cu_q.dim() != 1 or cu_q.numel() < 2:
+    qs, ks = q.shape, k.shape
+    if len(qs) != 3 or len(ks) != 3 or ks[2] != qs[2]:
+        raise ValueError(f"q {tuple(qs)} and k {tuple(ks)} must be [Tq, Hq, d] and [Tk, Hkv, d]")
+    _heads(qs[1], ks[1])
+    if not isinstance(cu_q, torch.Tensor) or cu_q.dim() != 1 or cu_q.shape[0] < 2:
+        _need(cu_q, "cu_q", _I32)
         raise ValueError("cu_q must hold the starts of the sequences and the end of the last one")
-    qs, ks = q.stride(), k.stride()
-    vs, os = ks if v is None else v.stride(), qs if o is None else o.stride()
-    return PromptParams(cu_q.numel() - 1, Hq, Hkv, d, Tq, Tk, _DTYPES[dt], 1 if causal else 0,
-                        1.0 / math.sqrt(d) if softmax_scale is None else softmax_scale,
-                        qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os[0], os[1])
+    ends = cu_q.shape
+    return dt, qs, ks, ends[0] - 1, _flat(cu_q, "cu_q", _I32, ends, dev), _flat(cu_k, "cu_k", _I32, ends, dev)
 
 
 def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor, cu_k: torch.Tensor, *,
@@ -102,20 +122,29 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
     keys j <= i + n_k - n_q (causal) or all of them.  Returns (O [Tq, Hq, d], lse
     [Hq, Tq] fp32); a row without keys is 0 with lse -inf.  Rows that belong to
     no sequence are not written (undefined unless ``out`` and ``lse`` are given)."""
-    if not isinstance(v, torch.Tensor):
-        raise TypeError("v must be a torch.Tensor")
-    O = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None and isinstance(q, torch.Tensor) else out
-    p = _prompt_params(q, k, v, O, cu_q, cu_k, causal, softmax_scale)
+    dev = _device()
+    dt, qs, ks, nseq, cq, ck = _prompt_shapes(q, k, cu_q, cu_k, dev)
+    (Tq, Hq, d), (Tk, Hkv, _) = qs, ks
+    qp, q0, q1 = _rows(q, "q", dt, qs, dev)
+    kp, k0, k1 = _rows(k, "k", dt, ks, dev)
+    vp, v0, v1 = _rows(v, "v", dt, ks, dev)
+    if out is None:
+        out = q.new_empty(qs)
+    op, o0, o1 = _rows(out, "out", dt, qs, dev)
     if lse is None:
-        lse = torch.empty((p.Hq, p.Tq), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((Hq, Tq), dtype=_F32)
+        lp = lse.data_ptr()
     else:
-        _need(lse, "lse", torch.float32, (p.Hq, p.Tq))
-    _on_current(q, k, v, cu_q, cu_k, O, lse)
-    L, ref = lib(), ctypes.byref(p)
-    ws, nws = _work_area(workspace, L.instagen_prompt_attention_workspace_size(ref), q, "instagen_prompt_attention")
-    _check(L.instagen_prompt_attention(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_q), _ptr(cu_k), ref, _ptr(O), _ptr(lse),
-                                       _ptr(ws), nws, _stream()), "instagen_prompt_attention")
-    return O, lse
+        lp = _flat(lse, "lse", _F32, (Hq, Tq), dev)
+    L = lib()
+    p = _prompt_block(nseq, Hq, Hkv, d, Tq, Tk, _DTYPES[dt], 1 if causal else 0,
+                      d ** -0.5 if softmax_scale is None else softmax_scale, q0, q1, k0, k1, v0, v1, o0, o1)
+    workspace, ws, nws = _work_area(workspace, L.instagen_prompt_attention_workspace_size(p), q, dev,
+                                    "instagen_prompt_attention")
+    rc = L.instagen_prompt_attention(qp, kp, vp, cq, ck, p, op, lp, ws, nws, _stream(dev))
+    if rc:
+        _check(rc, "instagen_prompt_attention")
+    return out, lse
 
 
 def key_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, cu_q: torch.Tensor, cu_k: torch.Tensor,
@@ -125,14 +154,21 @@ def key_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, cu_q: torch
     attention, summed over the queries that see it and the heads that share it
     (instagen_key_weights).  lse [Hq, Tq]: as ``prompt_attention`` returned it
     for these queries.  Returns weights."""
-    p = _prompt_params(q, k, None, None, cu_q, cu_k, causal, softmax_scale)
-    _need(lse, "lse", torch.float32, (p.Hq, p.Tq))
-    _need(weights, "weights", torch.float32, (p.Hkv, p.Tk))
-    _on_current(q, k, lse, cu_q, cu_k, weights)
-    L, ref = lib(), ctypes.byref(p)
-    ws, nws = _work_area(workspace, L.instagen_key_weights_workspace_size(ref), q, "instagen_key_weights")
-    _check(L.instagen_key_weights(_ptr(q), _ptr(k), _ptr(lse), _ptr(cu_q), _ptr(cu_k), ref, _ptr(weights), _ptr(ws),
-                                  nws, _stream()), "instagen_key_weights")
+    dev = _device()
+    dt, qs, ks, nseq, cq, ck = _prompt_shapes(q, k, cu_q, cu_k, dev)
+    (Tq, Hq, d), (Tk, Hkv, _) = qs, ks
+    qp, q0, q1 = _rows(q, "q", dt, qs, dev)
+    kp, k0, k1 = _rows(k, "k", dt, ks, dev)
+    lp = _flat(lse, "lse", _F32, (Hq, Tq), dev)
+    wp = _flat(weights, "weights", _F32, (Hkv, Tk), dev)
+    L = lib()
+    p = _prompt_block(nseq, Hq, Hkv, d, Tq, Tk, _DTYPES[dt], 1 if causal else 0,
+                      d ** -0.5 if softmax_scale is None else softmax_scale, q0, q1, k0, k1, k0, k1, q0, q1)
+    workspace, ws, nws = _work_area(workspace, L.instagen_key_weights_workspace_size(p), q, dev,
+                                    "instagen_key_weights")
+    rc = L.instagen_key_weights(qp, kp, lp, cq, ck, p, wp, ws, nws, _stream(dev))
+    if rc:
+        _check(rc, "instagen_key_weights")
     return weights
 
 
@@ -147,51 +183,51 @@ def prefix_attention(q: torch.Tensor, k_prefix: Optional[torch.Tensor], v_prefix
     of which lens [B] int32 are live.  With weights [B, Hkv, cap] fp32 the
     token's attention weights on its own keys are added to them.  Returns
     (O [B, Hq, d], lse [B, Hq] fp32)."""
+    dev = _device()
     dt = _dtype_of(q, "q")
-    B, Hkv, cap, d = _cache_shape(k_cache, "k_cache", dt)
-    _need(v_cache, "v_cache", dt, k_cache.shape)
-    if q.dim() != 3 or q.shape[0] != B or q.shape[2] != d:
-        raise ValueError(f"q has shape {tuple(q.shape)}, expected ({B}, Hq, {d})")
-    _need_rows(q, "q", dt, q.shape)
-    Hq = q.shape[1]
-    if Hq > 1 and q.stride(1) != d:
+    cs = _cache_shape(k_cache, "k_cache", dt)
+    B, Hkv, cap, d = cs
+    kc, vc = _flat(k_cache, "k_cache", dt, cs, dev), _flat(v_cache, "v_cache", dt, cs, dev)
+    qs = q.shape
+    if len(qs) != 3 or qs[0] != B or qs[2] != d:
+        raise ValueError(f"q has shape {tuple(qs)}, expected ({B}, Hq, {d})")
+    Hq = qs[1]
+    _heads(Hq, Hkv)
+    qp, q0, q1 = _rows(q, "q", dt, qs, dev)
+    if Hq > 1 and q1 != d:
         raise ValueError("q: the heads of a token must be contiguous")
-    if Hkv < 1 or Hq < 1 or Hq % Hkv:
-        raise ValueError(f"{Hq} query heads cannot share {Hkv} key/value heads")
     if (k_prefix is None) != (v_prefix is None):
         raise ValueError("k_prefix and v_prefix come together")
-    P, ph = 0, 0
+    P, kp, vp, ph = 0, None, None, 0
     if k_prefix is not None:
         if not isinstance(k_prefix, torch.Tensor) or k_prefix.dim() != 3:
             raise ValueError("k_prefix must be a tensor [Hkv, P, d]")
         P = k_prefix.shape[1]
-        _need_rows(k_prefix, "k_prefix", dt, (Hkv, P, d))
-        _need_rows(v_prefix, "v_prefix", dt, (Hkv, P, d))
-        ph = k_prefix.stride(0)
-        if P > 1 and (k_prefix.stride(1) != d or v_prefix.stride(1) != d):
+        kp, ph, k1 = _rows(k_prefix, "k_prefix", dt, (Hkv, P, d), dev)
+        vp, vh, v1 = _rows(v_prefix, "v_prefix", dt, (Hkv, P, d), dev)
+        if P > 1 and (k1 != d or v1 != d):
             raise ValueError("k_prefix, v_prefix: the rows of a head must be contiguous")
-        if Hkv > 1 and P > 0 and v_prefix.stride(0) != ph:
+        if Hkv > 1 and P > 0 and vh != ph:
             raise ValueError("k_prefix and v_prefix must have the same strides")
-    _need(lens, "lens", torch.int32, (B,))
-    if weights is not None:
-        _need(weights, "weights", torch.float32, (B, Hkv, cap))
+    np = _flat(lens, "lens", _I32, (B,), dev)
+    wp = None if weights is None else _flat(weights, "weights", _F32, (B, Hkv, cap), dev)
     if out is None:
-        out = torch.empty((B, Hq, d), dtype=dt, device=q.device)
+        out = q.new_empty(qs)
+        op = out.data_ptr()
     else:
-        _need(out, "out", dt, (B, Hq, d))
+        op = _flat(out, "out", dt, qs, dev)
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((B, Hq), dtype=_F32)
+        lp = lse.data_ptr()
     else:
-        _need(lse, "lse", torch.float32, (B, Hq))
-    _on_current(q, k_prefix, v_prefix, k_cache, v_cache, lens, weights, out, lse)
-    p = CacheParams(B, Hq, Hkv, d, P, cap, _DTYPES[dt], 1.0 / math.sqrt(d) if softmax_scale is None else softmax_scale,
-                    q.stride(0), ph)
-    L, ref = lib(), ctypes.byref(p)
-    ws, nws = _work_area(workspace, L.instagen_prefix_attention_workspace_size(ref, weights is not None), q,
-                         "instagen_prefix_attention")
-    _check(L.instagen_prefix_attention(_ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ptr(k_cache), _ptr(v_cache),
-                                       _ptr(lens), ref, _ptr(out), _ptr(lse), _ptr(weights), _ptr(ws), nws,
-                                       _stream()), "instagen_prefix_attention")
+        lp = _flat(lse, "lse", _F32, (B, Hq), dev)
+    L = lib()
+    p = _cache_block(B, Hq, Hkv, d, P, cap, _DTYPES[dt], d ** -0.5 if softmax_scale is None else softmax_scale, q0, ph)
+    workspace, ws, nws = _work_area(workspace, L.instagen_prefix_attention_workspace_size(p, wp is not None), q, dev,
+                                    "instagen_prefix_attention")
+    rc = L.instagen_prefix_attention(qp, kp, vp, kc, vc, np, p, op, lp, wp, ws, nws, _stream(dev))
+    if rc:
+        _check(rc, "instagen_prefix_attention")
     return out, lse
 
 
@@ -203,31 +239,32 @@ def evict(k_cache: torch.Tensor, v_cache: torch.Tensor, weights: torch.Tensor, p
     fp32, pos [B, Hkv, cap] int32, lens [B] int32.  In place, or into ``out``:
     (k, v, weights, pos, lens) with their own number of slots.  Returns the
     five evicted tensors."""
+    dev = _device()
     dt = _dtype_of(k_cache, "k_cache")
-    B, Hkv, cap, d = _cache_shape(k_cache, "k_cache", dt)
-    _need(v_cache, "v_cache", dt, k_cache.shape)
-    _need(weights, "weights", torch.float32, (B, Hkv, cap))
-    _need(pos, "pos", torch.int32, (B, Hkv, cap))
-    _need(lens, "lens", torch.int32, (B,))
+    cs = _cache_shape(k_cache, "k_cache", dt)
+    B, Hkv, cap, d = cs
+    ins = (_flat(k_cache, "k_cache", dt, cs, dev), _flat(v_cache, "v_cache", dt, cs, dev),
+           _flat(weights, "weights", _F32, (B, Hkv, cap), dev), _flat(pos, "pos", _I32, (B, Hkv, cap), dev),
+           _flat(lens, "lens", _I32, (B,), dev))
     if out is None:
-        out, cap_out = (k_cache, v_cache, weights, pos, lens), cap
+        out, outs, cap_out = (k_cache, v_cache, weights, pos, lens), ins, cap
     else:
         ko, vo, wo, po, lo = out
-        cap_out = _cache_shape(ko, "out[0]", dt)[2]
-        _need(ko, "out[0]", dt, (B, Hkv, cap_out, d))
-        _need(vo, "out[1]", dt, (B, Hkv, cap_out, d))
-        _need(wo, "out[2]", torch.float32, (B, Hkv, cap_out))
-        _need(po, "out[3]", torch.int32, (B, Hkv, cap_out))
-        _need(lo, "out[4]", torch.int32, (B,))
+        os = _cache_shape(ko, "out[0]", dt)
+        cap_out = os[2]
+        os = (B, Hkv, cap_out, d)
+        outs = (_flat(ko, "out[0]", dt, os, dev), _flat(vo, "out[1]", dt, os, dev),
+                _flat(wo, "out[2]", _F32, (B, Hkv, cap_out), dev), _flat(po, "out[3]", _I32, (B, Hkv, cap_out), dev),
+                _flat(lo, "out[4]", _I32, (B,), dev))
     if not 1 <= budget <= cap_out:
         raise ValueError(f"budget must be within [1, {cap_out}], got {budget}")
     if recent < 0:
         raise ValueError(f"recent must be >= 0, got {recent}")
-    _on_current(k_cache, v_cache, weights, pos, lens, *out)
-    p = CacheParams(B, Hkv, Hkv, d, 0, cap, _DTYPES[dt], 1.0, Hkv * d, 0)
-    L, ref = lib(), ctypes.byref(p)
-    ws, nws = _work_area(workspace, L.instagen_evict_workspace_size(ref, budget), k_cache, "instagen_evict")
-    _check(L.instagen_evict(_ptr(k_cache), _ptr(v_cache), _ptr(weights), _ptr(pos), _ptr(lens), ref, budget,
-                            min(recent, 2 ** 31 - 1), _ptr(out[0]), _ptr(out[1]), _ptr(out[2]), _ptr(out[3]),
-                            _ptr(out[4]), cap_out, _ptr(ws), nws, _stream()), "instagen_evict")
+    L = lib()
+    p = _cache_block(B, Hkv, Hkv, d, 0, cap, _DTYPES[dt], 1.0, Hkv * d, 0)
+    workspace, ws, nws = _work_area(workspace, L.instagen_evict_workspace_size(p, budget), k_cache, dev,
+                                    "instagen_evict")
+    rc = L.instagen_evict(*ins, p, budget, min(recent, 2 ** 31 - 1), *outs, cap_out, ws, nws, _stream(dev))
+    if rc:
+        _check(rc, "instagen_evict")
     return tuple(out)

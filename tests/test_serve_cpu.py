@@ -41,6 +41,14 @@ def test_struct_sizes(lib):
     assert ctypes.sizeof(ig.CacheParams) == 48 and ig.CacheParams.q_seq.offset == 32
 
 
+def test_packed_blocks_are_the_structs(lib):
+    from block_sparse_attention_head_b200 import serve
+    a = (3, 8, 2, 64, 100, 120, 1, 0, 0.125, *range(8, 72, 8))
+    assert serve._prompt_block(*a) == bytes(ig.PromptParams(*a))
+    a = (3, 8, 2, 64, 100, 50, 1, 0.125, 512, 6400)
+    assert serve._cache_block(*a) == bytes(ig.CacheParams(*a))
+
+
 BAD_PROMPTS = [
     (dict(nseq=0), INVALID), (dict(Hq=0), INVALID), (dict(Hkv=3), INVALID), (dict(Hkv=0), INVALID), (dict(d=96), UNSUPPORTED),
     (dict(Tq=-1), INVALID), (dict(Tk=-1), INVALID), (dict(dtype=2), INVALID), (dict(causal=2), INVALID),
