@@ -3,19 +3,23 @@
 //   see j of 2^(c q_i.k_j - lse_i log2(e)),  c = softmax_scale log2(e).
 //
 // The product is taken the other way round than for attention: S^T = K Q^T
-// puts the keys on the TMEM lanes, so a key's mass is summed by the one thread
-// that owns its lane, without atomics or shuffles, and nothing is written back
-// to TMEM.  A CTA owns 256 keys (two chains of M = 128 rows of K, on chip once)
-// and walks the tiles of 256 queries of one head that see them, head after
-// head; each Q tile is the B operand (N = 256) of both chains, which keeps the
-// shared-memory reads of an MMA below its tensor time (at N = 128 they are
-// equal).  lse comes through shared memory, converted once per tile to its
-// negative in log2 units (-inf for rows that see nothing or do not exist).
+// puts the keys on the TMEM lanes, so a key's mass is summed by the threads
+// that own its lane, without atomics or shuffles, and nothing is written back
+// to TMEM.  A CTA owns 256 keys (two chains of M = 128) and walks the tiles of
+// 128 queries of one head that see them, head after head.  The keys are the A
+// operand and stay in TMEM (written once), so that a product only reads the
+// query tile from shared memory, 64 bytes a cycle; with both operands there it
+// reads 128, all there is.  Three score tiles of 128 columns rotate between
+// the MMA warp and four warpgroups, each of which takes every fourth one:
+// product, load and exponentials of three visits overlap.  (Two warpgroups with
+// twice the registers and a whole row in them: 387 us for 2048 queries on 16384
+// keys, 32/4 heads, d = 128, against 362.)  lse comes through
+// shared memory, converted once per tile to its negative in log2 units (-inf
+// for rows that see nothing or do not exist).
 //
-// Bound: the exponentials, 2 * 2048 MUFU cycles per tile and CTA against 2 *
-// 1024 tensor cycles (d = 128); three eighths of those of unmasked tiles run
-// on the FMA pipe instead (degree 5: the sums keep fp32's digits).  Sixteen
-// warps share them, four per scheduler, two to a TMEM lane.
+// Bound: the exponentials, 2 * 1024 MUFU cycles per query tile and CTA against
+// 2 * 512 tensor cycles (d = 128); three eighths of those of unmasked tiles run
+// on the FMA pipe instead (degree 5: the sums keep fp32's digits).
 //
 // Few keys, many queries: nsplit CTAs share a key pair, each over its part of
 // the tiles, and add_parts_kernel adds their sums in order.
@@ -24,20 +28,22 @@
 namespace ig {
 
 namespace {
-constexpr int kKwThreads = 640;  // 16 warps of sums, 2 MMA, loader, lse
-constexpr int kKwTile = 256;   // keys per CTA, queries per tile
-constexpr int kKwLseRing = 4;
+constexpr int kKwThreads = 640;  // 16 warps of sums, MMA, spare, loader, lse
+constexpr int kKwKeys = 256;     // keys per CTA
+constexpr int kKwTile = 128;     // queries per tile
+constexpr int kKwStages = 6;     // query tiles on chip
+constexpr int kKwLse = 8;        // lse tiles
+// TMEM columns: the keys [0, 64) and [64, 128), three score tiles from 128 on
+constexpr uint32_t kKwS = 128;
 
 template <int D>
 struct KwSmem {
-  static constexpr int kKeyBytes = D * 256;   // 128 keys
-  static constexpr int kQBytes = D * 512;     // 256 queries
-  static constexpr int kK = 0;
-  static constexpr int kQ = kK + 2 * kKeyBytes;
-  static constexpr int kLse = kQ + 2 * kQBytes;
-  static constexpr int kXch = kLse + kKwLseRing * kKwTile * 4;  // the second half rows' sums
+  static constexpr int kQBytes = D * 256;  // 128 queries
+  static constexpr int kQ = 0;
+  static constexpr int kLse = kQ + kKwStages * kQBytes;
+  static constexpr int kXch = kLse + kKwLse * kKwTile * 4;  // sums of the second warpgroup of a chain
   static constexpr int kBars = kXch + 256 * 4;
-  static constexpr int kMisc = kBars + 24 * 8;
+  static constexpr int kMisc = kBars + 48 * 8;
   static constexpr int kBytes = kMisc + 64;
   static constexpr size_t bytes() { return 1024 + kBytes; }
 };
@@ -52,11 +58,13 @@ struct KwArgs {
   float* parts;  // [nsplit, Hkv, Tk] when nsplit > 1
   int nseq, Hkv, G, Tq, Tk, causal, nsplit, npair;
   float scale_log2;
+  const void* K;
+  int64_t k_tok, k_head;
 };
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kKwThreads, 1)
-    key_weights_kernel(KwArgs a, const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k) {
+    key_weights_kernel(KwArgs a, const __grid_constant__ CUtensorMap tmap_q) {
   using L = KwSmem<D>;
   constexpr bool kHalf = std::is_same<T, __half>::value;
   extern __shared__ uint8_t smem_raw[];
@@ -64,14 +72,14 @@ __global__ void __launch_bounds__(kKwThreads, 1)
   float* nlse = reinterpret_cast<float*>(smem + L::kLse);
   float* xch = reinterpret_cast<float*>(smem + L::kXch);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
-  uint64_t* k_full = bars + 0;
-  uint64_t* q_full = bars + 1;   // [2] stages
-  uint64_t* q_empty = bars + 3;  // [2]
-  uint64_t* s_full = bars + 5;   // [2] chains
-  uint64_t* s_empty = bars + 7;  // [2]
-  uint64_t* l_full = bars + 9;   // [kKwLseRing]
-  uint64_t* l_empty = bars + 13; // [kKwLseRing]
-  uint64_t* fin = bars + 17;     // [2] chains
+  uint64_t* k_ready = bars + 0;
+  uint64_t* fin = bars + 1;
+  uint64_t* s_full = bars + 2;                     // [4] warpgroups: the visit's scores are there
+  uint64_t* s_empty = bars + 6;                    // [3] score tiles
+  uint64_t* q_full = bars + 9;                     // [kKwStages]
+  uint64_t* q_empty = q_full + kKwStages;          // [kKwStages]
+  uint64_t* l_full = q_empty + kKwStages;          // [kKwLse]
+  uint64_t* l_empty = l_full + kKwLse;             // [kKwLse]
   int* misc = reinterpret_cast<int*>(smem + L::kMisc);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(misc + 0);
   volatile int* abort_flag = misc + 1;
@@ -94,7 +102,7 @@ __global__ void __launch_bounds__(kKwThreads, 1)
   clamp_rows(q0s, q1s, a.Tq);
   clamp_rows(k0s, k1s, a.Tk);
   const int nq = q1s - q0s, nk = k1s - k0s;
-  const int kb = local * kKwTile;  // first key of the pair
+  const int kb = local * kKwKeys;  // first key of the pair
   if (kb >= nk) return;
   const int off = nk - nq;         // causal: query i sees key j iff i >= j - off
   const int i0 = a.causal ? max(0, kb - off) / kKwTile : 0;
@@ -104,17 +112,17 @@ __global__ void __launch_bounds__(kKwThreads, 1)
   const int nv = v1 - v0;
 
   if (tid == 0) {
-    mbar_init(k_full, 1);
-    for (int i = 0; i < 2; ++i) {
+    mbar_init(k_ready, 256);
+    mbar_init(fin, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&s_full[i], 1);
+    for (int i = 0; i < 3; ++i) mbar_init(&s_empty[i], 128);
+    for (int i = 0; i < kKwStages; ++i) {
       mbar_init(&q_full[i], 1);
-      mbar_init(&q_empty[i], 2);
-      mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 256);
-      mbar_init(&fin[i], 1);
+      mbar_init(&q_empty[i], 1);
     }
-    for (int i = 0; i < kKwLseRing; ++i) {
+    for (int i = 0; i < kKwLse; ++i) {
       mbar_init(&l_full[i], 32);
-      mbar_init(&l_empty[i], 512);
+      mbar_init(&l_empty[i], 256);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -127,90 +135,101 @@ __global__ void __launch_bounds__(kKwThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  const uint32_t k_s = smem_u32(smem + L::kK), q_s = smem_u32(smem + L::kQ);
+  const uint32_t q_s = smem_u32(smem + L::kQ);
 
   float acc = 0.f;
   if (warp == 18) {
     // ================================================================ loader
-    if (lane == 0 && nv > 0) {
-      mbar_arrive_expect_tx(k_full, 2 * L::kKeyBytes);
-      for (int t = 0; t < 2; ++t)
-        for (int c = 0; c < D / 64; ++c)
-          tma_load_3d(k_s + t * L::kKeyBytes + c * 16384, &tmap_k, 64 * c, k0s + kb + 128 * t, hk, k_full);
-    }
     int issued = 0;
     for (int i = 0; i < nv; ++i) {
-      const int st = i & 1, v = v0 + i;
-      if (i >= 2 && !mbar_wait_warp(&q_empty[st], ((i >> 1) - 1) & 1, abort_flag)) break;
+      const int st = i % kKwStages, v = v0 + i;
+      if (i >= kKwStages && !mbar_wait_warp(&q_empty[st], (i / kKwStages - 1) & 1, abort_flag)) break;
       if (lane == 0) {
         const int row = q0s + (i0 + v % ntile) * kKwTile, head = hk * a.G + v / ntile;
         mbar_arrive_expect_tx(&q_full[st], L::kQBytes);
         for (int c = 0; c < D / 64; ++c)
-          tma_load_3d(q_s + st * L::kQBytes + c * 32768, &tmap_q, 64 * c, row, head, &q_full[st]);
+          tma_load_3d(q_s + st * L::kQBytes + c * 16384, &tmap_q, 64 * c, row, head, &q_full[st]);
       }
       issued = i + 1;
     }
-    if (nv > 0) mbar_wait_drain(k_full, 0);  // no copy in flight is left behind
-    for (int i = max(0, issued - 2); i < issued; ++i) mbar_wait_drain(&q_full[i & 1], (i >> 1) & 1);
+    for (int i = max(0, issued - kKwStages); i < issued; ++i)  // no copy in flight is left behind
+      mbar_wait_drain(&q_full[i % kKwStages], (i / kKwStages) & 1);
   } else if (warp == 19) {
     // =================================================================== lse
     for (int i = 0; i < nv; ++i) {
-      const int st = i % kKwLseRing, v = v0 + i;
+      const int st = i % kKwLse, v = v0 + i;
       const int tok = (i0 + v % ntile) * kKwTile, head = hk * a.G + v / ntile;
-      float x[8];
+      float x[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
+      for (int e = 0; e < 4; ++e) {
         const int row = tok + lane + 32 * e;
         const float y = row < nq ? __ldg(a.lse + (size_t)head * a.Tq + q0s + row) : -INFINITY;
         x[e] = y == -INFINITY ? -INFINITY : -y * kLog2E;
       }
-      if (i >= kKwLseRing && !mbar_wait_warp(&l_empty[st], (i / kKwLseRing - 1) & 1, abort_flag)) break;
+      if (i >= kKwLse && !mbar_wait_warp(&l_empty[st], (i / kKwLse - 1) & 1, abort_flag)) break;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) nlse[st * kKwTile + lane + 32 * e] = x[e];
+      for (int e = 0; e < 4; ++e) nlse[st * kKwTile + lane + 32 * e] = x[e];
       mbar_arrive(&l_full[st]);
     }
   } else if (warp >= 16) {
     // =================================================================== MMA
-    const int t = warp - 16;
-    const uint32_t idesc = umma_idesc_f16kind(128, 256, false, false, kHalf);
-    const uint64_t kd = umma_desc_sw128(k_s + t * L::kKeyBytes, 16, 1024);
-    const uint64_t qd0 = umma_desc_sw128(q_s, 16, 1024);
-    const uint32_t s_t = tmem + 256 * t;
-    bool ok = nv == 0 || mbar_wait_warp(k_full, 0, abort_flag);
-    for (int i = 0; i < nv && ok; ++i) {
-      ok = mbar_wait_warp(&q_full[i & 1], (i >> 1) & 1, abort_flag) &&
-           (i == 0 || mbar_wait_warp(&s_empty[t], (i - 1) & 1, abort_flag));
-      if (!ok) break;
-      tc_fence_after();
-      const uint64_t qd = qd0 + (uint64_t)(i & 1) * (uint64_t)(L::kQBytes >> 4);
-      if (elect_one()) {
+    // visit v: tile v / 2 of the list, chain v % 2, score tile v % 3
+    if (warp == 16) {
+      const uint32_t idesc = umma_idesc_f16kind(128, 128, false, false, kHalf);
+      const uint64_t qd0 = umma_desc_sw128(q_s, 16, 1024);
+      bool ok = nv == 0 || mbar_wait_warp(k_ready, 0, abort_flag);
+      for (int v = 0; v < 2 * nv && ok; ++v) {
+        const int i = v >> 1, st = i % kKwStages, b = v % 3;
+        if (!(v & 1)) ok = mbar_wait_warp(&q_full[st], (i / kKwStages) & 1, abort_flag);
+        if (ok && v >= 3) ok = mbar_wait_warp(&s_empty[b], (v / 3 - 1) & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t qd = qd0 + (uint64_t)st * (uint64_t)(L::kQBytes >> 4);
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          umma_bf16_ss(s_t, kd + (uint64_t)((k >> 2) * 1024 + (k & 3) * 2), qd + (uint64_t)((k >> 2) * 2048 + (k & 3) * 2),
-                       idesc, k > 0 ? 1u : 0u);
-        umma_commit(&s_full[t]);
-        umma_commit(&q_empty[i & 1]);
+          for (int k = 0; k < D / 16; ++k)
+            umma_f16_ts(tmem + kKwS + 128 * b, tmem + 64 * (v & 1) + 8 * k, qd + (uint64_t)((k >> 2) * 1024 + (k & 3) * 2),
+                        idesc, k > 0 ? 1u : 0u);
+          umma_commit(&s_full[v & 3]);
+          if (v & 1) umma_commit(&q_empty[st]);
+        }
+        __syncwarp();
       }
+      if (elect_one()) umma_commit(fin);
       __syncwarp();
+      mbar_wait_drain(fin, 0);
     }
-    if (elect_one()) umma_commit(&fin[t]);
-    __syncwarp();
-    mbar_wait_drain(&fin[t], 0);
   } else {
     // ================================================================ sums
-    // four warpgroups: chain t's lanes, columns [128 half, 128 half + 128)
-    const int t = warp >> 3, half = (warp >> 2) & 1, qd = warp & 3;
+    // warpgroup w: visits v = w mod 4, so chain w % 2 and every other tile
+    const int t = (warp >> 2) & 1, half = warp >> 3, qd = warp & 3;
     const int key = kb + 128 * t + 32 * qd + lane;
-    const uint32_t s_col = tmem + (uint32_t)((32 * qd) << 16) + 256 * t + 128 * half;
+    const uint32_t lane_off = (uint32_t)((32 * qd) << 16);
+    if (half == 0) {  // the chain's keys into TMEM: two elements to a column
+      const int row = min(k0s + key, a.Tk - 1);  // (rows past the end are garbage that is not summed)
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.K) + row * a.k_tok + hk * a.k_head);
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        uint4 v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = __ldg(src + 8 * c + e);
+        tmem_st32(tmem + lane_off + 64 * t + 32 * c, reinterpret_cast<const float*>(v));
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(k_ready);
+    }
     const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
-    for (int i = 0; i < nv; ++i) {
-      const int tok = (i0 + (v0 + i) % ntile) * kKwTile + 128 * half;
-      // columns [lo, hi) of the half tile: queries that exist and see this key
+    for (int i = half; i < nv; i += 2) {
+      const int v = 2 * i + t, b = v % 3;
+      const int tok = (i0 + (v0 + i) % ntile) * kKwTile;
+      // columns [lo, hi) of the tile: queries that exist and see this key
       const int lo = a.causal ? key - off - tok : 0, hi = nq - tok;
       const bool whole = hi >= 128 && (!a.causal || kb + 128 * t + 127 - off <= tok);
-      const float* nl = nlse + (i % kKwLseRing) * kKwTile + 128 * half;
-      if (!mbar_wait_warp(&l_full[i % kKwLseRing], (i / kKwLseRing) & 1, abort_flag)) break;
-      if (!mbar_wait_warp(&s_full[t], i & 1, abort_flag)) break;
+      const float* nl = nlse + (i % kKwLse) * kKwTile;
+      const uint32_t s_col = tmem + lane_off + kKwS + 128 * b;
+      if (!mbar_wait_warp(&l_full[i % kKwLse], (i / kKwLse) & 1, abort_flag)) break;
+      if (!mbar_wait_warp(&s_full[v & 3], (i >> 1) & 1, abort_flag)) break;
       tc_fence_after();
       uint64_t sum[2] = {0ull, 0ull};
       auto chunk = [&](int c, float (&v)[32], auto masked) {
@@ -240,21 +259,26 @@ __global__ void __launch_bounds__(kKwThreads, 1)
         }
       };
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        float x[32];
-        tmem_ld32(s_col + 32 * c, x);
+      for (int c = 0; c < 2; ++c) {
+        float x0[32], x1[32];
+        tmem_ld32(s_col + 64 * c, x0);
+        tmem_ld32(s_col + 64 * c + 32, x1);
         tmem_wait_ld();
-        pin_regs32(x);
-        if (c == 3) {
+        pin_regs32(x0);
+        pin_regs32(x1);
+        if (c == 1) {
           tc_fence_before();
-          mbar_arrive(&s_empty[t]);
+          mbar_arrive(&s_empty[b]);
         }
-        if (whole)
-          chunk(c, x, std::false_type());
-        else
-          chunk(c, x, std::true_type());
+        if (whole) {
+          chunk(2 * c, x0, std::false_type());
+          chunk(2 * c + 1, x1, std::false_type());
+        } else {
+          chunk(2 * c, x0, std::true_type());
+          chunk(2 * c + 1, x1, std::true_type());
+        }
       }
-      mbar_arrive(&l_empty[i % kKwLseRing]);
+      mbar_arrive(&l_empty[i % kKwLse]);
       float s0, s1;
       unpack2(add2(sum[0], sum[1]), s0, s1);
       acc += s0 + s1;
@@ -263,8 +287,8 @@ __global__ void __launch_bounds__(kKwThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp < 16 && !((warp >> 2) & 1)) {
-    const int lane_t = 128 * (warp >> 3) + 32 * (warp & 3) + lane;
+  if (warp < 8) {
+    const int lane_t = 128 * (warp >> 2) + 32 * (warp & 3) + lane;
     if (kb + lane_t < nk) {
       const size_t at = (size_t)hk * a.Tk + k0s + kb + lane_t;
       acc += xch[lane_t];
@@ -299,14 +323,21 @@ __global__ void __launch_bounds__(256) add_parts_kernel(KwArgs a) {
   a.weights[at] += s;
 }
 
-// CTAs per key pair: where the pairs leave SMs idle, the visits are split so
-// that about every SM has a CTA, in parts of at least 2.
+// CTAs per key pair: the visits of a pair are split where that shortens the
+// whole: waves of CTAs times a CTA's visits and the 6 that its start and end
+// cost, in parts of at least 4 visits.
 static int key_weight_splits(const PromptArgs& a) {
   const long long ctas = row_pairs(a.Tk, 1, a.nseq) * a.Hkv;
   const long long visits = (long long)a.G * ((a.Tq / a.nseq + kKwTile - 1) / kKwTile);
-  long long n = ctas >= kSms ? 1 : kSms / ctas;
-  if (n > visits / 2) n = visits / 2;
-  return n < 1 ? 1 : (int)n;
+  long long best = 1, cost = -1;
+  for (long long n = 1; n <= 64 && (n == 1 || visits / n >= 4); ++n) {
+    const long long c = (ctas * n + kSms - 1) / kSms * ((visits + n - 1) / n + 6);
+    if (cost < 0 || c < cost) {
+      best = n;
+      cost = c;
+    }
+  }
+  return (int)best;
 }
 
 size_t key_weights_ws(const PromptArgs& a) {
@@ -315,11 +346,11 @@ size_t key_weights_ws(const PromptArgs& a) {
 }
 
 template <typename T, int D>
-static cudaError_t run_key_weights(const KwArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, cudaStream_t s) {
+static cudaError_t run_key_weights(const KwArgs& a, const CUtensorMap& tq, cudaStream_t s) {
   const size_t sm = KwSmem<D>::bytes();
   cudaError_t e = cudaFuncSetAttribute(key_weights_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
   if (e != cudaSuccess) return e;
-  key_weights_kernel<T, D><<<(unsigned)((long long)a.npair * a.Hkv * a.nsplit), kKwThreads, sm, s>>>(a, tq, tk);
+  key_weights_kernel<T, D><<<(unsigned)((long long)a.npair * a.Hkv * a.nsplit), kKwThreads, sm, s>>>(a, tq);
   return cudaGetLastError();
 }
 
@@ -339,14 +370,16 @@ cudaError_t launch_key_weights(const PromptArgs& p, cudaStream_t s) {
   a.nsplit = key_weight_splits(p);
   a.npair = (int)row_pairs(p.Tk, 1, p.nseq);
   a.parts = static_cast<float*>(p.ws);
-  CUtensorMap tq, tk;
-  cudaError_t e = make_tmap_rows(&tq, p.Q, p.dtype, p.d, p.Tq, p.Hq, p.q_tok, p.q_head, 256);
-  if (e == cudaSuccess) e = make_tmap_rows(&tk, p.K, p.dtype, p.d, p.Tk, p.Hkv, p.k_tok, p.k_head, 128);
+  a.K = p.K;
+  a.k_tok = p.k_tok;
+  a.k_head = p.k_head;
+  CUtensorMap tq;
+  cudaError_t e = make_tmap_rows(&tq, p.Q, p.dtype, p.d, p.Tq, p.Hq, p.q_tok, p.q_head);
   if (e != cudaSuccess) return e;
   if (p.dtype == IG_BF16)
-    e = p.d == 128 ? run_key_weights<__nv_bfloat16, 128>(a, tq, tk, s) : run_key_weights<__nv_bfloat16, 64>(a, tq, tk, s);
+    e = p.d == 128 ? run_key_weights<__nv_bfloat16, 128>(a, tq, s) : run_key_weights<__nv_bfloat16, 64>(a, tq, s);
   else
-    e = p.d == 128 ? run_key_weights<__half, 128>(a, tq, tk, s) : run_key_weights<__half, 64>(a, tq, tk, s);
+    e = p.d == 128 ? run_key_weights<__half, 128>(a, tq, s) : run_key_weights<__half, 64>(a, tq, s);
   if (e != cudaSuccess || a.nsplit == 1) return e;
   add_parts_kernel<<<(unsigned)(((size_t)a.Hkv * a.Tk + 255) / 256), 256, 0, s>>>(a);
   return cudaGetLastError();
