@@ -1,24 +1,31 @@
 // Eviction from the caches by accumulated attention weight (instagen_evict).
 //
-// Two launches.  evict_select_kernel, one CTA per (sequence, head): every slot
-// gets a 32-bit key whose order is the order of eviction (recent, weight), and
-// a radix select finds the key at the budget and how many of the slots equal
-// to it stay (the lowest).  Weights and positions are read once into shared
-// memory (twice the positions: the recent ones are known once the newest is);
-// a pass counts one byte of the keys, lanes with equal bytes adding together,
-// because weights share their exponents.  Then each warp walks a contiguous
-// range of slots and, from the counts of the ranges before, lists the freed
-// slots below the budget and the kept slots from the budget on.
-// evict_move_kernel copies rows: the n-th of those into the n-th of these (in
-// place), or every kept row (into another cache); it is bound by the rows'
-// bytes.  Sources are at or above the budget and destinations below it, so
-// moving in place has no order.
+// Two launches.  evict_select_kernel, one cluster of S CTAs per (sequence,
+// head), each owning the r-th part of the slots: every slot gets a 32-bit key
+// whose order is the order of eviction (recent, weight), and a radix select
+// finds the key at the budget and how many of the slots equal to it stay (the
+// lowest).  Weights and positions are read once, into registers and from them
+// into shared memory; a pass counts one byte of the keys (in the first
+// one lanes with equal bytes add together, because weights share their
+// exponents) and the CTAs of a cluster add their counts through distributed
+// shared memory.  Then each
+// warp walks a contiguous range of slots and, from the counts of the ranges
+// before, lists the freed slots below the budget and the kept slots from the
+// budget on.  The pass over the slots is a chain of latencies, so S grows (to
+// 8) while there are SMs without a CTA: 64 caches of 16384 keys take 18 us in
+// clusters of 4 and 37 alone.  evict_move_kernel copies rows: the n-th of those
+// into the n-th of these (in place), or every kept row (into another cache); it
+// is bound by the rows' bytes.  Sources are at or above the budget and
+// destinations below it, so moving in place has no order.
 #include "serve.cuh"
+
+#include <cooperative_groups.h>
 
 namespace ig {
 
 namespace {
-constexpr int kEvictKeys = 49152;  // keys held in shared memory; longer caches are read again in every pass
+constexpr int kEvictKeys = 49152;  // keys held in a CTA's shared memory; longer parts are read again in every pass
+constexpr int kEvictBatch = 8;     // slots a thread loads at once
 constexpr int kEvictMoveThreads = 256;
 constexpr int kEvictMoveRows = 4;  // rows a thread copies, all loads in flight at once
 
@@ -56,105 +63,170 @@ __host__ __device__ inline EvictLists carve(void* ws, int B, int Hkv, int budget
   return l;
 }
 
-// kHeld: the keys fit shared memory.
+// kHeld: the keys of a CTA's part fit shared memory.
 template <bool kHeld>
 __global__ void __launch_bounds__(1024) evict_select_kernel(EvictArgs a) {
+  namespace cg = cooperative_groups;
   extern __shared__ uint32_t held[];
-  __shared__ int hist[256];
+  __shared__ int own[256];      // a pass's counts
+  __shared__ int all[2][256];   // and the cluster's, alternating: zeroed a pass ahead
   __shared__ int sums[32];
+  __shared__ int share[4];      // what the peers read: newest, recent slots, and the walk's counts
+  __shared__ int part[8][2];
   __shared__ uint32_t s_prefix;
-  __shared__ int s_need, s_equal, s_newest, s_safe;
-  const int bh = blockIdx.x, b = bh / a.Hkv, nt = blockDim.x;
+  __shared__ int s_need, s_equal;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int S = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int bh = blockIdx.x / S, b = bh / a.Hkv, nt = blockDim.x;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const EvictLists l = carve(a.ws, a.B, a.Hkv, a.budget);
   const int n = live_slots(a.lens, b, a.cap);
-  if (tid == 0 && bh % a.Hkv == 0) l.n[b] = n;
   int32_t* dst = l.dst + (size_t)bh * a.budget;
   int32_t* src = l.src + (size_t)bh * a.budget;
-  if (n <= a.budget) {  // everything stays
+  launch_dependents();
+  if (tid == 0 && rank == 0 && bh % a.Hkv == 0) l.n[b] = n;
+  if (n <= a.budget) {  // everything stays (all CTAs of the cluster leave here)
     if (!a.in_place)
-      for (int i = tid; i < n; i += nt) src[i] = i;
-    if (tid == 0) l.count[bh] = a.in_place ? 0 : n;
+      for (int i = rank * nt + tid; i < n; i += S * nt) src[i] = i;
+    if (tid == 0 && rank == 0) l.count[bh] = a.in_place ? 0 : n;
     return;
   }
-  const float* w = a.weights + (size_t)bh * a.cap;
-  const int32_t* pos = a.pos + (size_t)bh * a.cap;
+  // this CTA's slots [c0, c1), a whole number of warp steps but for the last
+  const int per = (n + 32 * S - 1) / (32 * S) * 32;
+  const int c0 = min(n, rank * per), c1 = min(n, c0 + per), cn = c1 - c0;
+  const float* w = a.weights + (size_t)bh * a.cap + c0;
+  const int32_t* pos = a.pos + (size_t)bh * a.cap + c0;
+  // the sum (or maximum) over the cluster of one value per CTA
+  auto cluster_all = [&](int v, int slot, bool maximum) -> int {
+    if (tid == 0) share[slot] = v;
+    if (S == 1) {
+      __syncthreads();
+      return share[slot];
+    }
+    cluster.sync();
+    int all = maximum ? INT32_MIN : 0;
+    for (int r = 0; r < S; ++r) {
+      const int x = *cluster.map_shared_rank(&share[slot], r);
+      all = maximum ? max(all, x) : all + x;
+    }
+    return all;
+  };
+  auto block_reduce = [&](int v, bool maximum) -> int {  // in thread 0
+    v = maximum ? __reduce_max_sync(0xffffffffu, v) : __reduce_add_sync(0xffffffffu, v);
+    __syncthreads();
+    if (lane == 0) sums[warp] = v;
+    __syncthreads();
+    v = lane < (nt >> 5) ? sums[lane] : maximum ? INT32_MIN : 0;
+    return maximum ? __reduce_max_sync(0xffffffffu, v) : __reduce_add_sync(0xffffffffu, v);
+  };
 
-  // the recent slots: pos > newest - recent
+  // weights and positions on their way together; short parts stay in registers
+  float w0[kEvictBatch];
+  int32_t p0[kEvictBatch];
   int newest = INT32_MIN;
-#pragma unroll 8
-  for (int i = tid; i < n; i += nt) newest = max(newest, pos[i]);
-  newest = __reduce_max_sync(0xffffffffu, newest);
+#pragma unroll
+  for (int e = 0; e < kEvictBatch; ++e) {
+    const int i = tid + e * nt;
+    w0[e] = i < cn ? w[i] : 0.f;
+    p0[e] = i < cn ? pos[i] : INT32_MIN;
+  }
+#pragma unroll
+  for (int e = 0; e < kEvictBatch; ++e) newest = max(newest, p0[e]);
+#pragma unroll 4
+  for (int i = tid + kEvictBatch * nt; i < cn; i += nt) newest = max(newest, pos[i]);
   if (tid == 0) {
-    s_newest = INT32_MIN;
-    s_safe = 0;
     s_need = a.budget;
     s_prefix = 0;
   }
-  __syncthreads();
-  if (lane == 0) atomicMax(&s_newest, newest);
-  __syncthreads();
-  const long long edge = (long long)s_newest - a.recent;
+  for (int i = tid; i < 256; i += nt) all[0][i] = 0;
+  newest = cluster_all(block_reduce(newest, true), 0, true);
+  // the recent slots: pos > newest - recent
+  const long long edge = (long long)newest - a.recent;
   int safe = 0;
-#pragma unroll 8
-  for (int i = tid; i < n; i += nt) safe += pos[i] > edge;
-  safe = __reduce_add_sync(0xffffffffu, safe);
-  if (lane == 0) atomicAdd(&s_safe, safe);
-  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < kEvictBatch; ++e) safe += tid + e * nt < cn && p0[e] > edge;
+#pragma unroll 4
+  for (int i = tid + kEvictBatch * nt; i < cn; i += nt) safe += pos[i] > edge;
+  safe = cluster_all(block_reduce(safe, false), 1, false);
   // either there are enough recent slots and the others are below all of
   // them, or the recent ones are above all others
-  const bool among_safe = s_safe >= a.budget;
-  auto read_key = [&](int i) -> uint32_t {
-    const uint32_t key = ordered_bits(w[i]);
-    return (pos[i] > edge) == among_safe ? key : among_safe ? 0u : 0xffffffffu;
+  const bool among_safe = safe >= a.budget;
+  auto make_key = [&](float x, int32_t at) -> uint32_t {
+    return (at > edge) == among_safe ? ordered_bits(x) : among_safe ? 0u : 0xffffffffu;
   };
   if (kHeld) {
-#pragma unroll 8
-    for (int i = tid; i < n; i += nt) held[i] = read_key(i);
-    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < kEvictBatch; ++e)
+      if (tid + e * nt < cn) held[tid + e * nt] = make_key(w0[e], p0[e]);
+#pragma unroll 4
+    for (int i = tid + kEvictBatch * nt; i < cn; i += nt) held[i] = make_key(w[i], pos[i]);
   }
-  auto key_at = [&](int i) -> uint32_t { return kHeld ? held[i] : read_key(i); };
+  auto key_at = [&](int i) -> uint32_t { return kHeld ? held[i] : make_key(w[i], pos[i]); };
 
   // radix select: after a pass, s_prefix holds the leading bytes of the key
   // at the budget, s_equal how many slots share them and s_need how many of
-  // those stay; done when all of them do
+  // those stay; done when all of them do.  Every CTA of the cluster finds the
+  // same.
   uint32_t mask = 0;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256; i += nt) hist[i] = 0;
-    __syncthreads();
-    const uint32_t prefix = s_prefix;
-    for (int i0 = warp * 32; i0 < n; i0 += nt) {
-      const int i = i0 + lane;
-      const uint32_t key = i < n ? key_at(i) : 0u;
-      const bool in = i < n && (key & mask) == prefix;
-      const int digit = in ? (int)((key >> shift) & 255) : 256;
-      const unsigned peers = __match_any_sync(0xffffffffu, digit);
-      if (in && lane == __ffs(peers) - 1) atomicAdd(&hist[digit], __popc(peers));
+  for (int shift = 24, pass = 0; shift >= 0; shift -= 8, ++pass) {
+    // (the next pass's total is zeroed before this pass's cluster.sync, which
+    // every peer's additions to it come after; the first one before the syncs
+    // above)
+    for (int i = tid; i < 256; i += nt) {
+      own[i] = 0;
+      all[(pass & 1) ^ 1][i] = 0;
     }
     __syncthreads();
+    const uint32_t prefix = s_prefix;
+    for (int i0 = warp * 32; i0 < cn; i0 += nt) {
+      const int i = i0 + lane;
+      const uint32_t key = i < cn ? key_at(i) : 0u;
+      const bool in = i < cn && (key & mask) == prefix;
+      const int digit = (int)((key >> shift) & 255);
+      if (pass > 0) {
+        if (in) atomicAdd(&own[digit], 1);
+        continue;
+      }
+      // sign and exponent: a warp holds few different ones, each added once
+      const unsigned peers = __match_any_sync(0xffffffffu, in ? digit : 256);
+      if (in && lane == __ffs(peers) - 1) atomicAdd(&own[digit], __popc(peers));
+    }
+    __syncthreads();
+    const int* total = own;
+    if (S > 1) {  // every CTA adds its counts to every CTA's total
+      total = all[pass & 1];
+      for (int i = tid; i < 256; i += nt)
+        if (own[i])
+          for (int r = 0; r < S; ++r) atomicAdd(cluster.map_shared_rank(&all[pass & 1][i], r), own[i]);
+      cluster.sync();
+    }
     if (warp == 0) {  // the largest byte whose count from above reaches need
-      int own = 0;
+      int c[8], mine = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) own += hist[255 - (8 * lane + e)];
-      int incl = own;
+      for (int e = 0; e < 8; ++e) {
+        c[e] = total[255 - (8 * lane + e)];
+        mine += c[e];
+      }
+      int incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += y;
       }
       const int need = s_need;
-      int run = incl - own;
+      int run = incl - mine;
       __syncwarp();
       if (run < need && need <= incl) {
+        bool found = false;
+#pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const int byte = 255 - (8 * lane + e);
-          if (run + hist[byte] >= need) {
-            s_prefix = prefix | ((uint32_t)byte << shift);
+          if (!found && run + c[e] >= need) {
+            s_prefix = prefix | ((uint32_t)(255 - (8 * lane + e)) << shift);
             s_need = need - run;
-            s_equal = hist[byte];
-            break;
+            s_equal = c[e];
+            found = true;
           }
-          run += hist[byte];
+          run += c[e];
         }
       }
     }
@@ -166,15 +238,26 @@ __global__ void __launch_bounds__(1024) evict_select_kernel(EvictArgs a) {
   const int equal_kept = s_need;
   const bool all_equal = s_need == s_equal;
 
-  // ordered walk: every warp owns a contiguous range of slots
-  const int nw = nt >> 5, seg = (n + 32 * nw - 1) / (32 * nw) * 32;
-  const int i0 = min(n, warp * seg), i1 = min(n, i0 + seg);
+  // ordered walk: every warp owns a contiguous range of the CTA's slots
+  const int nw = nt >> 5, seg = (cn + 32 * nw - 1) / (32 * nw) * 32;
+  const int i0 = min(cn, warp * seg), i1 = min(cn, i0 + seg);
   const unsigned below = (1u << lane) - 1;
+  // what the CTAs before this one count
+  auto ranks_before = [&](int v, int slot) -> int {
+    if (S == 1) return 0;
+    if (tid == 0) share[slot] = v;
+    cluster.sync();
+    int before = 0;
+    for (int r = 0; r < rank; ++r) before += *cluster.map_shared_rank(&share[slot], r);
+    return before;
+  };
   int equal_before = 0;
   if (!all_equal) {
     int equal = 0;
     for (int i = i0 + lane; i < i1; i += 32) equal += (key_at(i) & mask) == level;
-    equal_before = warps_before(__reduce_add_sync(0xffffffffu, equal), sums);
+    equal = __reduce_add_sync(0xffffffffu, equal);
+    equal_before = warps_before(equal, sums);
+    equal_before += ranks_before(block_reduce(lane == 0 ? equal : 0, false), 2);
   }
   // f(slot, below the budget and freed, from the budget on and kept) for the
   // range's slots, 32 at a time
@@ -190,7 +273,7 @@ __global__ void __launch_bounds__(1024) evict_select_kernel(EvictArgs a) {
         if (key == level) kept = eq + __popc(same & below) < equal_kept;
         eq += __popc(same);
       }
-      f(i, i < i1 && !kept && i < a.budget, i < i1 && kept && i >= a.budget);
+      f(c0 + i, i < i1 && !kept && c0 + i < a.budget, i < i1 && kept && c0 + i >= a.budget);
     }
   };
   int freed = 0, moving = 0;
@@ -199,7 +282,22 @@ __global__ void __launch_bounds__(1024) evict_select_kernel(EvictArgs a) {
     moving += __popc(__ballot_sync(0xffffffffu, moves));
   });
   int f = warps_before(freed, sums), m = warps_before(moving, sums);
-  if (warp == nw - 1 && lane == 0) l.count[bh] = a.in_place ? f + freed : a.budget;
+  if (S > 1) {
+    // the CTAs' totals, both in one exchange
+    const int tf = block_reduce(lane == 0 ? freed : 0, false), tm = block_reduce(lane == 0 ? moving : 0, false);
+    if (tid == 0) {
+      share[0] = tf;
+      share[3] = tm;
+    }
+    cluster.sync();
+    if (tid < 2 * S) part[tid >> 1][tid & 1] = *cluster.map_shared_rank(&share[tid & 1 ? 3 : 0], tid >> 1);
+    __syncthreads();
+    for (int r = 0; r < rank; ++r) {
+      f += part[r][0];
+      m += part[r][1];
+    }
+  }
+  if (rank == S - 1 && warp == nw - 1 && lane == 0) l.count[bh] = a.in_place ? f + freed : a.budget;
   int32_t* from = a.in_place ? src : dst;  // out of place: dst is the list of the moving slots
   if (a.in_place) {
     each([&](int i, bool free, bool moves) {
@@ -210,18 +308,17 @@ __global__ void __launch_bounds__(1024) evict_select_kernel(EvictArgs a) {
       m += __popc(ms);
     });
   } else {
-    each([&](int i, bool, bool moves) {
-      const unsigned ms = __ballot_sync(0xffffffffu, moves);
+    // src of a slot that stays is itself, of the f-th freed one ~f: the move
+    // looks the f-th moving slot up
+    each([&](int i, bool free, bool moves) {
+      const unsigned fs = __ballot_sync(0xffffffffu, free), ms = __ballot_sync(0xffffffffu, moves);
       if (moves) from[m + __popc(ms & below)] = i;
+      if (i < c0 + i1 && i < a.budget) src[i] = free ? ~(f + __popc(fs & below)) : i;
+      f += __popc(fs);
       m += __popc(ms);
     });
-    __syncthreads();
-    each([&](int i, bool free, bool) {
-      const unsigned fs = __ballot_sync(0xffffffffu, free);
-      if (i < i1 && i < a.budget) src[i] = free ? from[f + __popc(fs & below)] : i;
-      f += __popc(fs);
-    });
   }
+  if (S > 1) cluster.sync();  // no CTA ends while a peer may still read its shared memory
 }
 
 template <int D>
@@ -230,6 +327,7 @@ __global__ void __launch_bounds__(kEvictMoveThreads) evict_move_kernel(EvictArgs
   constexpr int kGroup = kEvictMoveThreads / kLanes;   // rows at once
   const int bh = blockIdx.y, b = bh / a.Hkv;
   const EvictLists l = carve(a.ws, a.B, a.Hkv, a.budget);
+  wait_prior_grids();
   const int count = l.count[bh];
   if (blockIdx.x == 0 && bh % a.Hkv == 0 && threadIdx.x == 0) a.lens_out[b] = min(l.n[b], a.budget);
   const int32_t* dst = l.dst + (size_t)bh * a.budget;
@@ -243,7 +341,9 @@ __global__ void __launch_bounds__(kEvictMoveThreads) evict_move_kernel(EvictArgs
   for (int e = 0; e < kEvictMoveRows; ++e) {
     const int r = r0 + e * kGroup;
     if (r >= count) break;
-    const size_t from = in0 + src[r];
+    int s = src[r];
+    if (s < 0) s = dst[~s];  // a freed slot's number: the moving slot of that number
+    const size_t from = in0 + s;
     k[e] = static_cast<const uint4*>(a.K)[from * kLanes + c];
     v[e] = static_cast<const uint4*>(a.V)[from * kLanes + c];
     if (c == 0) {
@@ -270,27 +370,43 @@ size_t evict_ws(int B, int Hkv, int budget) {
   return ((size_t)B + (size_t)B * Hkv * (1 + 2 * (size_t)budget)) * 4;
 }
 
-cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
-  // short caches: several CTAs per SM; long ones: all of an SM's threads
-  const int threads = a.cap <= 4096 ? 256 : 1024;
-  cudaError_t e = cudaSuccess;
-  if (a.cap <= kEvictKeys) {
-    e = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvictKeys * 4);
+template <bool kHeld>
+static cudaError_t run_select(const EvictArgs& a, int S, int threads, size_t smem, cudaStream_t s) {
+  if (smem > 40 * 1024) {  // 48 KB with the static part need no leave
+    const cudaError_t e =
+        cudaFuncSetAttribute(evict_select_kernel<kHeld>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    evict_select_kernel<true><<<a.B * a.Hkv, threads, (size_t)a.cap * 4, s>>>(a);
-  } else {
-    evict_select_kernel<false><<<a.B * a.Hkv, threads, 0, s>>>(a);
   }
-  e = cudaGetLastError();
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)S;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(a.B * a.Hkv * S));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel<kHeld>, a);
+}
+
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
+  // CTAs per cache: doubled while there are SMs without one and a CTA's part
+  // is longer than 2048 slots
+  int S = 1;
+  while (S < 8 && 2 * S * a.B * a.Hkv <= 2 * kSms && a.cap / S > 2048) S *= 2;
+  const int per = (a.cap + 32 * S - 1) / (32 * S) * 32;
+  // short parts: several CTAs per SM; long ones: all of an SM's threads
+  const int threads = per <= 2048 ? 256 : per <= 4096 ? 512 : 1024;
+  cudaError_t e = per <= kEvictKeys ? run_select<true>(a, S, threads, (size_t)per * 4, s)
+                                    : run_select<false>(a, S, threads, 0, s);
   if (e != cudaSuccess) return e;
   const int rows = a.in_place ? min(a.budget, a.cap - a.budget) : a.budget;
   const int per_cta = kEvictMoveThreads / (a.d / 8) * kEvictMoveRows;
   const dim3 grid((unsigned)max(1, (rows + per_cta - 1) / per_cta), (unsigned)(a.B * a.Hkv));
-  if (a.d == 128)
-    evict_move_kernel<128><<<grid, kEvictMoveThreads, 0, s>>>(a);
-  else
-    evict_move_kernel<64><<<grid, kEvictMoveThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return a.d == 128 ? launch_after(evict_move_kernel<128>, grid, kEvictMoveThreads, 0, true, s, a)
+                    : launch_after(evict_move_kernel<64>, grid, kEvictMoveThreads, 0, true, s, a);
 }
 
 }  // namespace ig
