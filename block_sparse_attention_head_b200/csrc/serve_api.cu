@@ -60,7 +60,9 @@ int prompt_args(const instagen_prompt_params* p, ig::PromptArgs* a) {
   return IG_OK;
 }
 
+// (need = 256: the call uses none)
 bool good_ws(const void* ws, size_t have, size_t need) {
+  if (need == 256 && !ws) return true;
   return ws && have >= need && !(reinterpret_cast<uintptr_t>(ws) & 255u);
 }
 
@@ -187,7 +189,7 @@ size_t instagen_evict_workspace_size(const instagen_cache_params* p, int32_t bud
   ig::StepArgs a;
   if (step_args(p, &a) || budget < 1) return 0;
   const size_t n = ig::evict_ws(a.B, a.Hkv, budget);
-  return n < 256 ? 256 : n;
+  return n <= 256 ? 512 : n;  // (never the 256 of a call without scratch)
 }
 
 int instagen_evict(const void* K, const void* V, const float* weights, const int32_t* pos, const int32_t* lens,
@@ -204,7 +206,7 @@ int instagen_evict(const void* K, const void* V, const float* weights, const int
   if (!aligned16(K) || !aligned16(V) || !aligned16(K_out) || !aligned16(V_out)) return IG_ERR_INVALID_ARG;
   const int same = (K == K_out) + (V == V_out) + (weights == weights_out) + (pos == pos_out) + (lens == lens_out);
   if ((same != 0 && same != 5) || (same == 5 && cap_out != c.cap)) return IG_ERR_INVALID_ARG;
-  if (!good_ws(ws, ws_bytes, ig::evict_ws(c.B, c.Hkv, budget))) return IG_ERR_WORKSPACE;
+  if (!ws || !good_ws(ws, ws_bytes, instagen_evict_workspace_size(p, budget))) return IG_ERR_WORKSPACE;
   ig::EvictArgs a;
   a.K = K;
   a.V = V;

@@ -437,7 +437,7 @@ StepPlan step_plan(const StepArgs& a, bool with_weights) {
   p.lse_part = p.direct ? 0 : up(rows * nslot * a.d * 4);
   p.score = p.lse_part + (p.direct ? 0 : up(rows * nslot * 4));
   p.total = p.score + (with_weights ? up(rows * a.cap * 4) : 0);
-  if (p.total < 256) p.total = 256;
+  p.total = p.direct && !with_weights ? 256 : p.total < 512 ? 512 : p.total;  // 256: none needed
   return p;
 }
 
@@ -505,18 +505,20 @@ cudaError_t run_step(const StepArgs& s, const StepPlan& p, cudaStream_t st) {
       (long long)a.npre * a.Hkv + (long long)a.nown * a.Hkv * a.B * a.own_rows;
   if (ctas > 0) {
     CUtensorMap kp, vp, kc, vc;
-    // a map that no CTA uses needs an address all the same
+    // (a map that no CTA uses is a copy of the other)
     const bool pre = a.npre > 0, own = a.nown > 0;
-    e = make_tmap_rows(&kp, pre ? s.Kp : s.Q, s.dtype, D, pre ? s.P : 1, s.Hkv, D, pre ? s.prefix_head : D, kRowsKeys);
-    if (e == cudaSuccess)
-      e = make_tmap_rows(&vp, pre ? s.Vp : s.Q, s.dtype, D, pre ? s.P : 1, s.Hkv, D, pre ? s.prefix_head : D, kRowsKeys);
-    if (e == cudaSuccess)
-      e = make_tmap_rows(&kc, own ? s.Kc : s.Q, s.dtype, D, own ? s.cap : 1, s.B * s.Hkv, D,
-                         own ? (int64_t)s.cap * D : D, kRowsKeys);
-    if (e == cudaSuccess)
-      e = make_tmap_rows(&vc, own ? s.Vc : s.Q, s.dtype, D, own ? s.cap : 1, s.B * s.Hkv, D,
-                         own ? (int64_t)s.cap * D : D, kRowsKeys);
+    e = cudaSuccess;
+    if (pre) {
+      e = make_tmap_rows(&kp, s.Kp, s.dtype, D, s.P, s.Hkv, D, s.prefix_head, kRowsKeys);
+      if (e == cudaSuccess) e = make_tmap_rows(&vp, s.Vp, s.dtype, D, s.P, s.Hkv, D, s.prefix_head, kRowsKeys);
+    }
+    if (own && e == cudaSuccess) {
+      e = make_tmap_rows(&kc, s.Kc, s.dtype, D, s.cap, s.B * s.Hkv, D, (int64_t)s.cap * D, kRowsKeys);
+      if (e == cudaSuccess) e = make_tmap_rows(&vc, s.Vc, s.dtype, D, s.cap, s.B * s.Hkv, D, (int64_t)s.cap * D, kRowsKeys);
+    }
     if (e != cudaSuccess) return e;
+    if (!pre) kp = kc, vp = vc;
+    if (!own) kc = kp, vc = vp;
     // by the longest share: 16 tiles and more stream
     const int share = max(a.nown ? s.cap / a.nown : 0, a.npre ? s.P / a.npre : 0);
     e = share >= 16 * kRowsKeys ? run_rows<T, D, true>(a, (unsigned)ctas, p.npre_tc > 0, kp, vp, kc, vc, st)

@@ -86,6 +86,8 @@ def _work_area(workspace: Optional[torch.Tensor], need: int, like: torch.Tensor,
     if need == 0:
         raise InstaGenError(f"invalid or unsupported parameters for {what}")
     if workspace is None:
+        if need == 256:  # the call needs no scratch
+            return None, None, 0
         workspace = like.new_empty((need,), dtype=_U8)
         return workspace, workspace.data_ptr(), need
     have = workspace.numel() * workspace.element_size()
@@ -129,8 +131,10 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
     kp, k0, k1 = _rows(k, "k", dt, ks, dev)
     vp, v0, v1 = _rows(v, "v", dt, ks, dev)
     if out is None:
-        out = q.new_empty(qs)
-    op, o0, o1 = _rows(out, "out", dt, qs, dev)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        op, o0, o1 = out.data_ptr(), Hq * d, d
+    else:
+        op, o0, o1 = _rows(out, "out", dt, qs, dev)
     if lse is None:
         lse = q.new_empty((Hq, Tq), dtype=_F32)
         lp = lse.data_ptr()
@@ -212,7 +216,7 @@ def prefix_attention(q: torch.Tensor, k_prefix: Optional[torch.Tensor], v_prefix
     np = _flat(lens, "lens", _I32, (B,), dev)
     wp = None if weights is None else _flat(weights, "weights", _F32, (B, Hkv, cap), dev)
     if out is None:
-        out = q.new_empty(qs)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
         op = out.data_ptr()
     else:
         op = _flat(out, "out", dt, qs, dev)

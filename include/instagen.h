@@ -366,7 +366,8 @@ int instagen_forward_layout_get(const instagen_params* p, instagen_forward_layou
  * on floats.  Pointers to 16-bit tensors, O and lse must be 16-byte aligned.
  * Workspaces are scratch: 256-byte aligned, no contents kept; calls that may
  * overlap on the GPU (two streams, two captured graphs) need one each.  A
- * size function returns 0 for invalid parameters and at least 256 otherwise.
+ * size function returns 0 for invalid parameters and at least 256 otherwise;
+ * 256 says that the call needs none (ws may then be NULL).
  */
 typedef enum { IG_BF16 = 0, IG_F16 = 1 } instagen_dtype;
 

@@ -75,8 +75,13 @@ def test_prompt_pointers_refused(lib):
     for kw in (dict(Q=None), dict(K=None), dict(V=None), dict(O=None), dict(cu=None), dict(Q=ODD), dict(K=ODD),
                dict(V=ODD), dict(O=ODD)):
         assert prompt_call(lib, p, **kw) == INVALID
-    for kw in (dict(ws=None), dict(ws=ODD), dict(n=need - 1)):
+    for kw in (dict(ws=ODD), dict(n=need - 1)):
         assert prompt_call(lib, p, **kw) == WORKSPACE
+    split = prompt(nseq=1, Tq=4, Tk=100000)  # few rows, many keys: parts are kept on the side
+    need = lib.instagen_prompt_attention_workspace_size(ctypes.byref(split))
+    assert need > 256
+    for kw in (dict(ws=None), dict(ws=ODD), dict(n=need - 1)):
+        assert prompt_call(lib, split, **kw) == WORKSPACE
     for kw in (dict(v_tok=60), dict(v_head=0), dict(o_tok=8), dict(o_head=1)):
         assert prompt_call(lib, prompt(**kw)) == INVALID
     assert lib.instagen_prompt_attention(FAKE, FAKE, FAKE, FAKE, FAKE, None, FAKE, None, FAKE, 1 << 40, None) == INVALID
