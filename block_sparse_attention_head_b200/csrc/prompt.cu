@@ -283,38 +283,36 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (warp >= 8) {
     setmaxnreg_dec<72>();
-    if (warp == 10) {
-      // ============================================================= loader
+    if (warp >= 10) {
+      // ============================================================ loaders
+      // warp 10 brings K, warp 11 V: a stage of K is free long before the V of
+      // the same tile, and with one row tile the next K is needed soon after
+      const bool is_v = warp == 11;
+      const CUtensorMap* map = is_v ? &tmap_v : &tmap_k;
+      uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
+      const uint32_t base = is_v ? v_s : k_s;
       int issued = 0;
       for (int i = 0; i < nj; ++i) {
         const int s = i & 1, row = k0s + (j0 + i) * 128;
-        if (i >= 2 && !mbar_wait_warp(&k_empty[s], ((i >> 1) - 1) & 1, abort_flag)) break;
+        if (i >= 2 && !mbar_wait_warp(&empty[s], ((i >> 1) - 1) & 1, abort_flag)) break;
         if (lane == 0) {
-          mbar_arrive_expect_tx(&k_full[s], L::kTileBytes);
+          mbar_arrive_expect_tx(&full[s], L::kTileBytes);
           for (int c = 0; c < D / 64; ++c)
-            tma_load_3d(k_s + s * L::kTileBytes + c * 16384, &tmap_k, 64 * c, row, hk, &k_full[s]);
+            tma_load_3d(base + s * L::kTileBytes + c * 16384, map, 64 * c, row, hk, &full[s]);
         }
-        if (i >= 2 && !mbar_wait_warp(&v_empty[s], ((i >> 1) - 1) & 1, abort_flag)) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&v_full[s], L::kTileBytes);
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_3d(v_s + s * L::kTileBytes + c * 16384, &tmap_v, 64 * c, row, hk, &v_full[s]);
-        }
-        if (j0 + i == cut) {  // zero the V rows behind the sequence's end
-          if (!mbar_wait_warp(&v_full[s], (i >> 1) & 1, abort_flag)) break;
+        issued = i + 1;
+        if (is_v && j0 + i == cut) {  // zero the V rows behind the sequence's end
+          mbar_wait_drain(&full[s], (i >> 1) & 1);
           for (int c = 0; c < D / 64; ++c)
             for (int b = (nk & 127) * 8 + lane; b < 1024; b += 32)
-              st_shared_v4(v_s + s * L::kTileBytes + c * 16384 + b * 16, 0u, 0u, 0u, 0u);
+              st_shared_v4(base + s * L::kTileBytes + c * 16384 + b * 16, 0u, 0u, 0u, 0u);
           fence_proxy_async_smem();
           mbar_arrive(v_fixed);
         }
-        issued = i + 1;
       }
-      for (int i = max(0, issued - 2); i < issued; ++i) {  // no copy in flight is left behind
-        mbar_wait_drain(&k_full[i & 1], (i >> 1) & 1);
-        mbar_wait_drain(&v_full[i & 1], (i >> 1) & 1);
-      }
-    } else if (warp < 10) {
+      for (int i = max(0, issued - 2); i < issued; ++i)  // no copy in flight is left behind
+        mbar_wait_drain(&full[i & 1], (i >> 1) & 1);
+    } else {
       // ================================================================ MMA
       // warp 8 + t issues chain t: S_t(first), then PV_t(previous), S_t(next),
       // ... PV_t(last); the warp waits in step, one elected lane issues
