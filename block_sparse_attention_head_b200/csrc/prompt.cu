@@ -133,7 +133,8 @@ struct TcArgs {
   const int32_t* cu_q;  // null: one sequence of Tq and Tk rows
   const int32_t* cu_k;
   int nseq, Hq, Hkv, G, Tq, Tk, causal, nsplit, ntile;
-  bool partial;  // write o_part / lse_part
+  bool partial;    // write o_part / lse_part
+  int short_last;  // > 0: pair numbers from here on are the sequences' last pairs of one row tile
   float scale_log2;
   int64_t q_tok, q_head, o_tok, o_head;
 };
@@ -218,7 +219,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // ---- which rows
   int q0s = 0, q1s = a.Tq, k0s = 0, k1s = a.Tk, local = t_glob;
   if (a.cu_q) {
-    if (warp == 0) {
+    if (a.short_last > 0 && t_glob >= a.short_last) {
+      if (tid == 0) {
+        const int s = t_glob - a.short_last;
+        *reinterpret_cast<SeqPair*>(work) = {s, 0, a.cu_q[s], a.cu_q[s + 1], a.cu_k[s], a.cu_k[s + 1]};
+      }
+    } else if (warp == 0) {
       const SeqPair p = find_pair(a.cu_q, a.cu_k, a.nseq, a.G, t_glob);
       if (lane == 0) *reinterpret_cast<SeqPair*>(work) = p;
     }
@@ -238,6 +244,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // the last rows of a sequence see the most keys: they go first
   const int pair = (R + kTcRows - 1) / kTcRows - 1 - local;
   if (pair < 0 || local < 0) return;
+  // a sequence's last pair of one row tile goes behind all others, if asked for
+  if (a.short_last > 0 && (t_glob >= a.short_last) != (local == 0 && R - pair * kTcRows <= 128)) return;
   const int r0 = pair * kTcRows;
   const int rows0 = min(128, R - r0), rows1 = max(0, min(128, R - r0 - 128));
   const bool one = rows1 == 0;  // one row tile: chains take the even / odd key tiles
@@ -788,6 +796,14 @@ cudaError_t launch_prompt_attention(const PromptArgs& p, cudaStream_t s) {
   a.o_head = p.o_head;
   a.ntile = (int)row_pairs(p.Tq, p.G, p.nseq);
   a.nsplit = prompt_splits(p);
+  // Long keys and few units: the sequences' last pairs, where they hold one row
+  // tile (half the time), start last and fill the end.  4 chunks of 257 rows
+  // on up to 8191 keys, 40 heads: 268 us against 280.  Each costs an idle CTA
+  // of a microsecond, so not with many short sequences.
+  if (a.nsplit == 1 && p.nseq * p.Hkv <= 2 * kSms && p.Tk / p.nseq >= 2048) {
+    a.short_last = a.ntile;
+    a.ntile += p.nseq;
+  }
   a.partial = a.nsplit > 1;
   a.o_part = static_cast<float*>(p.ws);
   a.lse_part = a.o_part + (size_t)a.nsplit * p.Tq * p.Hq * p.d;

@@ -116,6 +116,7 @@ PROMPTS = {
     "steps": ([1] * 33, [1 + 37 * i for i in range(33)], 16, 2, 128),
     "long": ([1500], [4100], 4, 2, 128),
     "long_few_rows": ([3], [9001], 5, 1, 64),
+    "ragged_last": ([257, 300], [2100, 2200], 50, 50, 64),
 }
 
 
