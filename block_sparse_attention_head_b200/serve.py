@@ -21,8 +21,13 @@ _prompt_block = struct.Struct("@8if4x8q").pack  # instagen_prompt_params
 _cache_block = struct.Struct("@7if2q").pack     # instagen_cache_params
 
 
-def _device() -> int:
-    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else torch.cuda.current_device()
+def _device(t, name: str) -> int:
+    """The current device, given that t is a CUDA tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise InstaGenError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    return torch._C._cuda_getDevice()
 
 
 def _stream(dev: int) -> int:
@@ -124,7 +129,7 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
     keys j <= i + n_k - n_q (causal) or all of them.  Returns (O [Tq, Hq, d], lse
     [Hq, Tq] fp32); a row without keys is 0 with lse -inf.  Rows that belong to
     no sequence are not written (undefined unless ``out`` and ``lse`` are given)."""
-    dev = _device()
+    dev = _device(q, "q")
     dt, qs, ks, nseq, cq, ck = _prompt_shapes(q, k, cu_q, cu_k, dev)
     (Tq, Hq, d), (Tk, Hkv, _) = qs, ks
     qp, q0, q1 = _rows(q, "q", dt, qs, dev)
@@ -158,7 +163,7 @@ def key_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, cu_q: torch
     attention, summed over the queries that see it and the heads that share it
     (instagen_key_weights).  lse [Hq, Tq]: as ``prompt_attention`` returned it
     for these queries.  Returns weights."""
-    dev = _device()
+    dev = _device(q, "q")
     dt, qs, ks, nseq, cq, ck = _prompt_shapes(q, k, cu_q, cu_k, dev)
     (Tq, Hq, d), (Tk, Hkv, _) = qs, ks
     qp, q0, q1 = _rows(q, "q", dt, qs, dev)
@@ -187,7 +192,7 @@ def prefix_attention(q: torch.Tensor, k_prefix: Optional[torch.Tensor], v_prefix
     of which lens [B] int32 are live.  With weights [B, Hkv, cap] fp32 the
     token's attention weights on its own keys are added to them.  Returns
     (O [B, Hq, d], lse [B, Hq] fp32)."""
-    dev = _device()
+    dev = _device(q, "q")
     dt = _dtype_of(q, "q")
     cs = _cache_shape(k_cache, "k_cache", dt)
     B, Hkv, cap, d = cs
@@ -243,7 +248,7 @@ def evict(k_cache: torch.Tensor, v_cache: torch.Tensor, weights: torch.Tensor, p
     fp32, pos [B, Hkv, cap] int32, lens [B] int32.  In place, or into ``out``:
     (k, v, weights, pos, lens) with their own number of slots.  Returns the
     five evicted tensors."""
-    dev = _device()
+    dev = _device(k_cache, "k_cache")
     dt = _dtype_of(k_cache, "k_cache")
     cs = _cache_shape(k_cache, "k_cache", dt)
     B, Hkv, cap, d = cs

@@ -359,7 +359,8 @@ int instagen_forward_layout_get(const instagen_params* p, instagen_forward_layou
  * multiply V are rounded to the tensors' type (each rounding at most half a
  * step of it), O once at the end; lse is the natural log of the sum of
  * exp(softmax_scale * q.k) and -inf for a row that sees no key, whose O is 0.
- * Contents of K and V rows behind a sequence's end (or past a cache's length)
+ * Outputs must not overlap inputs (weights is both, and so are evict's tensors
+ * in place).  Contents of K and V rows behind a sequence's end (or past a cache's length)
  * never matter, NaN included; values a sequence's own rows hold must be
  * finite (a non-finite V row may reach earlier rows of the same sequence
  * through a zero probability).  Results do not depend on timing: no atomics
@@ -418,7 +419,8 @@ typedef struct {
   int32_t B, Hq, Hkv, d;     /* sequences, heads (Hkv divides Hq, Hq / Hkv <= 1024),
                                 d in {64, 128}; B * Hkv <= 65535                      */
   int32_t P;                 /* keys of the prefix that all sequences share, >= 0     */
-  int32_t cap;               /* slots of each sequence's own cache, >= 0              */
+  int32_t cap;               /* slots of each sequence's own cache, >= 0 (attention:
+                                < 2^28)                                               */
   int32_t dtype;             /* instagen_dtype                                        */
   float softmax_scale;       /* logit scale > 0 (instagen_evict: not used)            */
   int64_t q_seq;             /* Q: elements from a sequence to the next (its Hq rows

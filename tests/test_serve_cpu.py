@@ -100,7 +100,7 @@ BAD_CACHES = [
     (dict(B=0), INVALID), (dict(Hkv=3), INVALID), (dict(d=32), UNSUPPORTED), (dict(P=-1), INVALID), (dict(cap=-1), INVALID),
     (dict(dtype=-1), INVALID), (dict(softmax_scale=0.0), INVALID), (dict(q_seq=500), INVALID), (dict(q_seq=516), INVALID),
     (dict(prefix_head=6392), INVALID), (dict(prefix_head=6404), INVALID), (dict(B=40000), UNSUPPORTED),
-    (dict(cap=2 ** 30), UNSUPPORTED), (dict(P=2 ** 31 - 1), UNSUPPORTED),
+    (dict(cap=2 ** 30), UNSUPPORTED), (dict(B=1, Hkv=1, cap=2 ** 28), UNSUPPORTED), (dict(P=2 ** 31 - 1), UNSUPPORTED),
 ]
 
 
@@ -149,3 +149,16 @@ def test_evict_refused(lib):
         assert call(outs=outs) == INVALID
     assert call(outs=[FAKE] * 5, cap_out=49) == INVALID  # in place keeps the slots
     assert call(cap_out=2 ** 31 - 1, budget=5) == UNSUPPORTED
+
+
+def test_binding_refuses_cpu_tensors(lib):
+    import torch
+    q, k = torch.zeros(8, 4, 64, dtype=torch.bfloat16), torch.zeros(8, 2, 64, dtype=torch.bfloat16)
+    c, n = torch.tensor([0, 8], dtype=torch.int32), torch.tensor([8], dtype=torch.int32)
+    kc, w, pos = k[None].transpose(1, 2).contiguous(), torch.zeros(1, 2, 8), torch.zeros(1, 2, 8, dtype=torch.int32)
+    for call in (lambda: ig.prompt_attention(q, k, k, c, c), lambda: ig.key_weights(q, k, w, c, c, w),
+                 lambda: ig.prefix_attention(q[:1], None, None, kc, kc, n), lambda: ig.evict(kc, kc, w, pos, n, 4, 1)):
+        with pytest.raises(ig.InstaGenError, match="CUDA tensor"):
+            call()
+    with pytest.raises(TypeError):
+        ig.prompt_attention(None, k, k, c, c)
