@@ -666,6 +666,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (warp == 9) wait_prior_grids();  // this grid's end is that of the one it overlaps, too
   if (warp == 8) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -751,12 +752,13 @@ static int key_splits(long long ctas, long long keys) {
 }
 
 template <typename T, int D>
-static cudaError_t run_attend(const TcArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+static cudaError_t run_attend(const TcArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s,
+                              bool overlap = false) {
   const size_t sm = TcSmem<D>::bytes();
   cudaError_t e = cudaFuncSetAttribute(attend_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
   if (e != cudaSuccess) return e;
-  attend_kernel<T, D><<<(unsigned)((long long)a.ntile * a.Hkv * a.nsplit), kTcThreads, sm, s>>>(a, tk, tv);
-  return cudaGetLastError();
+  return launch_after(attend_kernel<T, D>, dim3((unsigned)((long long)a.ntile * a.Hkv * a.nsplit)), kTcThreads, sm,
+                      overlap, s, a, tk, tv);
 }
 
 static cudaError_t dispatch_attend(const TcArgs& a, int dtype, int d, const CUtensorMap& tk, const CUtensorMap& tv,

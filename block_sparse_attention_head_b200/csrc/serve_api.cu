@@ -93,7 +93,6 @@ int step_attention_args(const instagen_cache_params* p, ig::StepArgs* a) {
   const int rc = step_args(p, a);
   if (rc) return rc;
   if (!good_scale(p->softmax_scale)) return IG_ERR_INVALID_ARG;
-  if (p->cap > (1 << 28) - 4096) return IG_ERR_UNSUPPORTED;  // grid.y of the weights' part
   if (a->q_seq < (int64_t)p->Hq * p->d || a->q_seq % 8 || a->q_seq > (int64_t(1) << 38)) return IG_ERR_INVALID_ARG;
   if (p->P > 0 && (a->prefix_head < (int64_t)p->P * p->d || a->prefix_head % 8 || a->prefix_head > (int64_t(1) << 38)))
     return IG_ERR_INVALID_ARG;

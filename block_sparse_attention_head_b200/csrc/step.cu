@@ -16,9 +16,10 @@
 //           the same launch.
 //   finish  join, and add the own keys' weights 2^(score - lse) from the scores
 //           that rows_kernel left (4 G bytes per key beside the 4 d it read).
-// The launches overlap: rows_kernel may start while attend_kernel's last CTAs
-// run (neither reads what the other writes), finish_kernel's CTAs wait where
-// they need the parts.
+// The launches overlap: the caches' CTAs go first, the prefix's take the SMs
+// that they leave (neither reads what the other writes), and finish_kernel's
+// CTAs wait where they need the parts.  (The prefix first, whose CTAs all end
+// together: 110 us against 102 for 128 sequences behind 32768 keys.)
 #include "serve.cuh"
 
 namespace ig {
@@ -26,7 +27,7 @@ namespace ig {
 namespace {
 constexpr int kRowsThreads = 160;  // 4 warps of 16 keys, 1 loader
 constexpr int kRowsKeys = 64;      // keys per tile
-constexpr int kFinishKeys = 4096;  // keys per CTA of the weights' part
+constexpr int kFinishKeys = 2048;  // keys that a CTA of the weights' part takes at a time
 
 // kLong: 96 KB in flight and two CTAs per SM, the faster stream; else 64 KB and
 // three CTAs, whose starts and ends hide one another, for short shares.
@@ -297,7 +298,6 @@ __global__ void __launch_bounds__(kRowsThreads, kLong ? 2 : 3)
         *reinterpret_cast<float2*>(ow + (warp * 16 + (lane >> 2) + 8 * h) * D + 8 * d + (lane & 3) * 2) =
             make_float2(o[d][2 * h] * w[h], o[d][2 * h + 1] * w[h]);
   }
-  wait_prior_grids();  // this grid's end is the prefix's, too
   named_bar_sync(1, 128);
   if (*abort_flag) return;
   for (int x = tid; x < 16 * (D / 4); x += 128) {
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kRowsThreads, kLong ? 2 : 3)
 }
 
 // blockIdx.y = 0 joins the parts of the G rows of one (sequence, key/value
-// head); the others add the weights of kFinishKeys of its own keys each.
+// head); the others share the weights of its own keys, kFinishKeys at a time.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) finish_kernel(RowsArgs a) {
   extern __shared__ float lse2[];  // [G]
@@ -342,16 +342,18 @@ __global__ void __launch_bounds__(256) finish_kernel(RowsArgs a) {
   const size_t rows = (size_t)a.B * a.Hq, row0 = (size_t)b * a.Hq + hk * a.G;
   const bool join = blockIdx.y == 0;
   const int n = join ? 0 : live_slots(a.lens, b, a.cap);
-  const int j0 = ((int)blockIdx.y - 1) * kFinishKeys;
+  const int j0 = ((int)blockIdx.y - 1) * kFinishKeys, jstep = ((int)gridDim.y - 1) * kFinishKeys;
   if (!join && j0 >= n) return;
   wait_prior_grids();
   for (int g = warp; g < a.G; g += 8) {
-    float top = -INFINITY, sum = 0.f;
-    for (int i = lane; i < a.nslot; i += 32) top = fmaxf(top, a.lse_part[i * rows + row0 + g]);
+    const float* lp = a.lse_part + row0 + g;
+    const float x0 = lane < a.nslot ? lp[lane * rows] : -INFINITY;
+    float top = x0, sum = 0.f;
+    for (int i = lane + 32; i < a.nslot; i += 32) top = fmaxf(top, lp[i * rows]);
 #pragma unroll
     for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    for (int i = lane; i < a.nslot; i += 32)
-      sum += top == -INFINITY ? 0.f : exp2f(a.lse_part[i * rows + row0 + g] - top);
+    sum = top == -INFINITY ? 0.f : exp2f(x0 - top);
+    for (int i = lane + 32; i < a.nslot; i += 32) sum += top == -INFINITY ? 0.f : exp2f(lp[i * rows] - top);
     sum = warp_sum(sum);
     const float y = sum == 0.f ? -INFINITY : top + log2f(sum);
     if (lane == 0) lse2[g] = y;
@@ -362,11 +364,11 @@ __global__ void __launch_bounds__(256) finish_kernel(RowsArgs a) {
     for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
     for (int i0 = 0; i0 < a.nslot; i0 += 32) {
       // lane i: the weight of part i0 + i (an empty part's rows were not written)
-      const float x = i0 + lane < a.nslot ? a.lse_part[(i0 + lane) * rows + row0 + g] : -INFINITY;
+      const float x = i0 == 0 ? x0 : i0 + lane < a.nslot ? lp[(i0 + lane) * rows] : -INFINITY;
       const float w = x == -INFINITY ? 0.f : exp2f(x - y);
       const unsigned some = __ballot_sync(0xffffffffu, x != -INFINITY);
       const int end = min(32, a.nslot - i0);
-#pragma unroll 4
+#pragma unroll 8
       for (int i = 0; i < end; ++i) {
         const float wi = __shfl_sync(0xffffffffu, w, i);
         const float* src = a.o_part + ((i0 + i) * rows + row0 + g) * D + lane * (D / 32);
@@ -387,19 +389,29 @@ __global__ void __launch_bounds__(256) finish_kernel(RowsArgs a) {
   __syncthreads();
   const float* score = a.score + (size_t)bh * a.G * a.cap;
   float* weights = a.weights + (size_t)bh * a.cap;
-  const int j1 = min(n, j0 + kFinishKeys);
-  for (int j = j0 + threadIdx.x; j < j1; j += 4 * 256) {
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+  // 8 keys a thread: their weights and two heads' scores in flight at once
+  constexpr int kKeys = kFinishKeys / 256;
+  const int j1 = n;
+  for (int j = j0 + threadIdx.x; j < n; j += jstep) {
+    float sum[kKeys], old[kKeys];
+#pragma unroll
+    for (int e = 0; e < kKeys; ++e) {
+      old[e] = j + 256 * e < j1 ? weights[j + 256 * e] : 0.f;
+      sum[e] = 0.f;
+    }
+#pragma unroll 2
     for (int g = 0; g < a.G; ++g) {
       const float y = lse2[g];
+      const float* sg = score + (size_t)g * a.cap;
+      float x[kKeys];
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (j + 256 * e < j1) sum[e] += ex2_approx(score[(size_t)g * a.cap + j + 256 * e] - y);
+      for (int e = 0; e < kKeys; ++e) x[e] = j + 256 * e < j1 ? sg[j + 256 * e] : -INFINITY;
+#pragma unroll
+      for (int e = 0; e < kKeys; ++e) sum[e] += ex2_approx(x[e] - y);
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (j + 256 * e < j1) weights[j + 256 * e] += sum[e];
+    for (int e = 0; e < kKeys; ++e)
+      if (j + 256 * e < j1) weights[j + 256 * e] = old[e] + sum[e];
   }
 }
 
@@ -442,13 +454,13 @@ StepPlan step_plan(const StepArgs& a, bool with_weights) {
 }
 
 template <typename T, int D, bool kLong>
-cudaError_t run_rows(const RowsArgs& a, unsigned ctas, bool after_prefix, const CUtensorMap& kp, const CUtensorMap& vp,
+cudaError_t run_rows(const RowsArgs& a, unsigned ctas, const CUtensorMap& kp, const CUtensorMap& vp,
                      const CUtensorMap& kc, const CUtensorMap& vc, cudaStream_t st) {
   const size_t sm = RowsSmem<D, kLong>::bytes();
   const cudaError_t e =
       cudaFuncSetAttribute(rows_kernel<T, D, kLong>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
   if (e != cudaSuccess) return e;
-  return launch_after(rows_kernel<T, D, kLong>, dim3(ctas), kRowsThreads, sm, after_prefix, st, a, kp, vp, kc, vc);
+  return launch_after(rows_kernel<T, D, kLong>, dim3(ctas), kRowsThreads, sm, false, st, a, kp, vp, kc, vc);
 }
 
 template <typename T, int D>
@@ -478,6 +490,30 @@ cudaError_t run_step(const StepArgs& s, const StepPlan& p, cudaStream_t st) {
   a.lse = s.lse;
   a.weights = s.weights;
   cudaError_t e;
+  const long long ctas =
+      (long long)a.npre * a.Hkv + (long long)a.nown * a.Hkv * a.B * a.own_rows;
+  if (ctas > 0) {
+    CUtensorMap kp, vp, kc, vc;
+    // (a map that no CTA uses is a copy of the other)
+    const bool pre = a.npre > 0, own = a.nown > 0;
+    e = cudaSuccess;
+    if (pre) {
+      e = make_tmap_rows(&kp, s.Kp, s.dtype, D, s.P, s.Hkv, D, s.prefix_head, kRowsKeys);
+      if (e == cudaSuccess) e = make_tmap_rows(&vp, s.Vp, s.dtype, D, s.P, s.Hkv, D, s.prefix_head, kRowsKeys);
+    }
+    if (own && e == cudaSuccess) {
+      e = make_tmap_rows(&kc, s.Kc, s.dtype, D, s.cap, s.B * s.Hkv, D, (int64_t)s.cap * D, kRowsKeys);
+      if (e == cudaSuccess) e = make_tmap_rows(&vc, s.Vc, s.dtype, D, s.cap, s.B * s.Hkv, D, (int64_t)s.cap * D, kRowsKeys);
+    }
+    if (e != cudaSuccess) return e;
+    if (!pre) kp = kc, vp = vc;
+    if (!own) kc = kp, vc = vp;
+    // by the longest share: more than 32 tiles stream
+    const int share = max(a.nown ? s.cap / a.nown : 0, a.npre ? s.P / a.npre : 0);
+    e = share > 32 * kRowsKeys ? run_rows<T, D, true>(a, (unsigned)ctas, kp, vp, kc, vc, st)
+                               : run_rows<T, D, false>(a, (unsigned)ctas, kp, vp, kc, vc, st);
+    if (e != cudaSuccess) return e;
+  }
   if (p.npre_tc) {
     TcArgs t{};
     t.Q = s.Q;
@@ -498,36 +534,15 @@ cudaError_t run_step(const StepArgs& s, const StepPlan& p, cudaStream_t st) {
     CUtensorMap tk, tv;
     e = make_tmap_rows(&tk, s.Kp, s.dtype, D, s.P, s.Hkv, D, s.prefix_head);
     if (e == cudaSuccess) e = make_tmap_rows(&tv, s.Vp, s.dtype, D, s.P, s.Hkv, D, s.prefix_head);
-    if (e == cudaSuccess) e = run_attend<T, D>(t, tk, tv, st);
-    if (e != cudaSuccess) return e;
-  }
-  const long long ctas =
-      (long long)a.npre * a.Hkv + (long long)a.nown * a.Hkv * a.B * a.own_rows;
-  if (ctas > 0) {
-    CUtensorMap kp, vp, kc, vc;
-    // (a map that no CTA uses is a copy of the other)
-    const bool pre = a.npre > 0, own = a.nown > 0;
-    e = cudaSuccess;
-    if (pre) {
-      e = make_tmap_rows(&kp, s.Kp, s.dtype, D, s.P, s.Hkv, D, s.prefix_head, kRowsKeys);
-      if (e == cudaSuccess) e = make_tmap_rows(&vp, s.Vp, s.dtype, D, s.P, s.Hkv, D, s.prefix_head, kRowsKeys);
-    }
-    if (own && e == cudaSuccess) {
-      e = make_tmap_rows(&kc, s.Kc, s.dtype, D, s.cap, s.B * s.Hkv, D, (int64_t)s.cap * D, kRowsKeys);
-      if (e == cudaSuccess) e = make_tmap_rows(&vc, s.Vc, s.dtype, D, s.cap, s.B * s.Hkv, D, (int64_t)s.cap * D, kRowsKeys);
-    }
-    if (e != cudaSuccess) return e;
-    if (!pre) kp = kc, vp = vc;
-    if (!own) kc = kp, vc = vp;
-    // by the longest share: 16 tiles and more stream
-    const int share = max(a.nown ? s.cap / a.nown : 0, a.npre ? s.P / a.npre : 0);
-    e = share >= 16 * kRowsKeys ? run_rows<T, D, true>(a, (unsigned)ctas, p.npre_tc > 0, kp, vp, kc, vc, st)
-                                : run_rows<T, D, false>(a, (unsigned)ctas, p.npre_tc > 0, kp, vp, kc, vc, st);
+    if (e == cudaSuccess) e = run_attend<T, D>(t, tk, tv, st, ctas > 0);
     if (e != cudaSuccess) return e;
   }
   if (p.direct && ctas > 0) return cudaSuccess;
-  const dim3 grid(s.B * s.Hkv, 1u + (s.weights ? (unsigned)((s.cap + kFinishKeys - 1) / kFinishKeys) : 0u));
-  return launch_after(finish_kernel<T, D>, grid, 256, s.G * 4, ctas > 0, st, a);
+  // the weights' CTAs: about what the SMs hold at once
+  const int caches = s.B * s.Hkv, chunks = (s.cap + kFinishKeys - 1) / kFinishKeys;
+  const int share = min(chunks, (4 * kSms + caches - 1) / caches);
+  const dim3 grid(caches, 1u + (s.weights ? (unsigned)share : 0u));
+  return launch_after(finish_kernel<T, D>, grid, 256, s.G * 4, ctas > 0 || p.npre_tc > 0, st, a);
 }
 }  // namespace
 

@@ -419,8 +419,7 @@ typedef struct {
   int32_t B, Hq, Hkv, d;     /* sequences, heads (Hkv divides Hq, Hq / Hkv <= 1024),
                                 d in {64, 128}; B * Hkv <= 65535                      */
   int32_t P;                 /* keys of the prefix that all sequences share, >= 0     */
-  int32_t cap;               /* slots of each sequence's own cache, >= 0 (attention:
-                                < 2^28)                                               */
+  int32_t cap;               /* slots of each sequence's own cache, >= 0              */
   int32_t dtype;             /* instagen_dtype                                        */
   float softmax_scale;       /* logit scale > 0 (instagen_evict: not used)            */
   int64_t q_seq;             /* Q: elements from a sequence to the next (its Hq rows

@@ -100,7 +100,7 @@ BAD_CACHES = [
     (dict(B=0), INVALID), (dict(Hkv=3), INVALID), (dict(d=32), UNSUPPORTED), (dict(P=-1), INVALID), (dict(cap=-1), INVALID),
     (dict(dtype=-1), INVALID), (dict(softmax_scale=0.0), INVALID), (dict(q_seq=500), INVALID), (dict(q_seq=516), INVALID),
     (dict(prefix_head=6392), INVALID), (dict(prefix_head=6404), INVALID), (dict(B=40000), UNSUPPORTED),
-    (dict(cap=2 ** 30), UNSUPPORTED), (dict(B=1, Hkv=1, cap=2 ** 28), UNSUPPORTED), (dict(P=2 ** 31 - 1), UNSUPPORTED),
+    (dict(cap=2 ** 30), UNSUPPORTED), (dict(P=2 ** 31 - 1), UNSUPPORTED),
 ]
 
 
