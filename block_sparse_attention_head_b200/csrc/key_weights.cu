@@ -13,7 +13,7 @@
 // the MMA warp and four warpgroups, each of which takes every fourth one:
 // product, load and exponentials of three visits overlap.  (Two warpgroups with
 // twice the registers and a whole row in them: 387 us for 2048 queries on 16384
-// keys, 32/4 heads, d = 128, against 362.)  lse comes through
+// keys, 32/4 heads, d = 128, against 356.)  lse comes through
 // shared memory, converted once per tile to its negative in log2 units (-inf
 // for rows that see nothing or do not exist).
 //
@@ -138,6 +138,7 @@ __global__ void __launch_bounds__(kKwThreads, 1)
   const uint32_t q_s = smem_u32(smem + L::kQ);
 
   float acc = 0.f;
+  if (warp >= 16) setmaxnreg_dec<64>();  // 4 * 32 * 64 + 16 * 32 * 104 = 640 * 96
   if (warp == 18) {
     // ================================================================ loader
     int issued = 0;
@@ -202,6 +203,7 @@ __global__ void __launch_bounds__(kKwThreads, 1)
   } else {
     // ================================================================ sums
     // warpgroup w: visits v = w mod 4, so chain w % 2 and every other tile
+    setmaxnreg_inc<104>();
     const int t = (warp >> 2) & 1, half = warp >> 3, qd = warp & 3;
     const int key = kb + 128 * t + 32 * qd + lane;
     const uint32_t lane_off = (uint32_t)((32 * qd) << 16);
@@ -258,7 +260,7 @@ __global__ void __launch_bounds__(kKwThreads, 1)
           }
         }
       };
-#pragma unroll 1
+#pragma unroll
       for (int c = 0; c < 2; ++c) {
         float x0[32], x1[32];
         tmem_ld32(s_col + 64 * c, x0);
