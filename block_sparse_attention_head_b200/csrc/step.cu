@@ -16,10 +16,11 @@
 //           the same launch.
 //   finish  join, and add the own keys' weights 2^(score - lse) from the scores
 //           that rows_kernel left (4 G bytes per key beside the 4 d it read).
-// The launches overlap: the caches' CTAs go first, the prefix's take the SMs
-// that they leave (neither reads what the other writes), and finish_kernel's
-// CTAs wait where they need the parts.  (The prefix first, whose CTAs all end
-// together: 110 us against 102 for 128 sequences behind 32768 keys.)
+// The launches overlap (neither of the two reads what the other writes), and
+// finish_kernel's CTAs wait where they need the parts.  The prefix goes first
+// where it leaves SMs for all of the caches' CTAs (32 sequences behind 4000
+// keys: 25 us against 33); else the caches do, and the prefix's CTAs take the
+// SMs as they come free (128 sequences behind 32768 keys: 102 us against 110).
 #include "serve.cuh"
 
 namespace ig {
@@ -298,6 +299,7 @@ __global__ void __launch_bounds__(kRowsThreads, kLong ? 2 : 3)
         *reinterpret_cast<float2*>(ow + (warp * 16 + (lane >> 2) + 8 * h) * D + 8 * d + (lane & 3) * 2) =
             make_float2(o[d][2 * h] * w[h], o[d][2 * h + 1] * w[h]);
   }
+  wait_prior_grids();  // this grid's end is that of the one it overlaps, too
   named_bar_sync(1, 128);
   if (*abort_flag) return;
   for (int x = tid; x < 16 * (D / 4); x += 128) {
@@ -454,13 +456,13 @@ StepPlan step_plan(const StepArgs& a, bool with_weights) {
 }
 
 template <typename T, int D, bool kLong>
-cudaError_t run_rows(const RowsArgs& a, unsigned ctas, const CUtensorMap& kp, const CUtensorMap& vp,
+cudaError_t run_rows(const RowsArgs& a, unsigned ctas, bool overlap, const CUtensorMap& kp, const CUtensorMap& vp,
                      const CUtensorMap& kc, const CUtensorMap& vc, cudaStream_t st) {
   const size_t sm = RowsSmem<D, kLong>::bytes();
   const cudaError_t e =
       cudaFuncSetAttribute(rows_kernel<T, D, kLong>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
   if (e != cudaSuccess) return e;
-  return launch_after(rows_kernel<T, D, kLong>, dim3(ctas), kRowsThreads, sm, false, st, a, kp, vp, kc, vc);
+  return launch_after(rows_kernel<T, D, kLong>, dim3(ctas), kRowsThreads, sm, overlap, st, a, kp, vp, kc, vc);
 }
 
 template <typename T, int D>
@@ -489,32 +491,9 @@ cudaError_t run_step(const StepArgs& s, const StepPlan& p, cudaStream_t st) {
   a.O = s.O;
   a.lse = s.lse;
   a.weights = s.weights;
-  cudaError_t e;
-  const long long ctas =
-      (long long)a.npre * a.Hkv + (long long)a.nown * a.Hkv * a.B * a.own_rows;
-  if (ctas > 0) {
-    CUtensorMap kp, vp, kc, vc;
-    // (a map that no CTA uses is a copy of the other)
-    const bool pre = a.npre > 0, own = a.nown > 0;
-    e = cudaSuccess;
-    if (pre) {
-      e = make_tmap_rows(&kp, s.Kp, s.dtype, D, s.P, s.Hkv, D, s.prefix_head, kRowsKeys);
-      if (e == cudaSuccess) e = make_tmap_rows(&vp, s.Vp, s.dtype, D, s.P, s.Hkv, D, s.prefix_head, kRowsKeys);
-    }
-    if (own && e == cudaSuccess) {
-      e = make_tmap_rows(&kc, s.Kc, s.dtype, D, s.cap, s.B * s.Hkv, D, (int64_t)s.cap * D, kRowsKeys);
-      if (e == cudaSuccess) e = make_tmap_rows(&vc, s.Vc, s.dtype, D, s.cap, s.B * s.Hkv, D, (int64_t)s.cap * D, kRowsKeys);
-    }
-    if (e != cudaSuccess) return e;
-    if (!pre) kp = kc, vp = vc;
-    if (!own) kc = kp, vc = vp;
-    // by the longest share: more than 32 tiles stream
-    const int share = max(a.nown ? s.cap / a.nown : 0, a.npre ? s.P / a.npre : 0);
-    e = share > 32 * kRowsKeys ? run_rows<T, D, true>(a, (unsigned)ctas, kp, vp, kc, vc, st)
-                               : run_rows<T, D, false>(a, (unsigned)ctas, kp, vp, kc, vc, st);
-    if (e != cudaSuccess) return e;
-  }
-  if (p.npre_tc) {
+  cudaError_t e = cudaSuccess;
+  // the prefix on the tensor cores
+  auto prefix = [&](bool overlap) -> cudaError_t {
     TcArgs t{};
     t.Q = s.Q;
     t.o_part = a.o_part;
@@ -532,9 +511,42 @@ cudaError_t run_step(const StepArgs& s, const StepPlan& p, cudaStream_t st) {
     t.q_tok = s.q_seq;
     t.q_head = D;
     CUtensorMap tk, tv;
-    e = make_tmap_rows(&tk, s.Kp, s.dtype, D, s.P, s.Hkv, D, s.prefix_head);
+    cudaError_t e = make_tmap_rows(&tk, s.Kp, s.dtype, D, s.P, s.Hkv, D, s.prefix_head);
     if (e == cudaSuccess) e = make_tmap_rows(&tv, s.Vp, s.dtype, D, s.P, s.Hkv, D, s.prefix_head);
-    if (e == cudaSuccess) e = run_attend<T, D>(t, tk, tv, st, ctas > 0);
+    return e != cudaSuccess ? e : run_attend<T, D>(t, tk, tv, st, overlap);
+  };
+  const long long ctas =
+      (long long)a.npre * a.Hkv + (long long)a.nown * a.Hkv * a.B * a.own_rows;
+  if (ctas > 0) {
+    CUtensorMap kp, vp, kc, vc;
+    // (a map that no CTA uses is a copy of the other)
+    const bool pre = a.npre > 0, own = a.nown > 0;
+    if (pre) {
+      e = make_tmap_rows(&kp, s.Kp, s.dtype, D, s.P, s.Hkv, D, s.prefix_head, kRowsKeys);
+      if (e == cudaSuccess) e = make_tmap_rows(&vp, s.Vp, s.dtype, D, s.P, s.Hkv, D, s.prefix_head, kRowsKeys);
+    }
+    if (own && e == cudaSuccess) {
+      e = make_tmap_rows(&kc, s.Kc, s.dtype, D, s.cap, s.B * s.Hkv, D, (int64_t)s.cap * D, kRowsKeys);
+      if (e == cudaSuccess) e = make_tmap_rows(&vc, s.Vc, s.dtype, D, s.cap, s.B * s.Hkv, D, (int64_t)s.cap * D, kRowsKeys);
+    }
+    if (e != cudaSuccess) return e;
+    if (!pre) kp = kc, vp = vc;
+    if (!own) kc = kp, vc = vp;
+    // by the longest share: more than 32 tiles stream
+    const int share = max(a.nown ? s.cap / a.nown : 0, a.npre ? s.P / a.npre : 0);
+    const bool stream = share > 32 * kRowsKeys;
+    // the prefix's CTAs take an SM each: they go first where the others leave
+    // room for all of the caches' CTAs beside them
+    const long long room = (kSms - (long long)p.npre_tc * row_pairs_one(s.B, s.G) * s.Hkv) * (stream ? 2 : 3);
+    const bool prefix_first = p.npre_tc > 0 && ctas <= room;
+    if (prefix_first) e = prefix(false);
+    if (e == cudaSuccess)
+      e = stream ? run_rows<T, D, true>(a, (unsigned)ctas, prefix_first, kp, vp, kc, vc, st)
+                 : run_rows<T, D, false>(a, (unsigned)ctas, prefix_first, kp, vp, kc, vc, st);
+    if (e == cudaSuccess && p.npre_tc > 0 && !prefix_first) e = prefix(true);
+    if (e != cudaSuccess) return e;
+  } else if (p.npre_tc > 0) {
+    e = prefix(false);
     if (e != cudaSuccess) return e;
   }
   if (p.direct && ctas > 0) return cudaSuccess;
