@@ -12,8 +12,8 @@
 //           16 keys of every 64-key tile with m16n8k16 products, whose score
 //           registers are the next product's operand registers, so scores
 //           never leave the registers; tiles stream through a TMA ring.  A
-//           prefix with at most 16 rows (small batches) goes the same way, in
-//           the same launch.
+//           prefix with at most 16 rows, or a short one that is read again for
+//           every 16 rows (kRowsPasses), goes the same way in the same launch.
 //   finish  join, and add the own keys' weights 2^(score - lse) from the scores
 //           that rows_kernel left (4 G bytes per key beside the 4 d it read).
 // The launches overlap (neither of the two reads what the other writes), and
@@ -28,6 +28,13 @@ namespace ig {
 namespace {
 constexpr int kRowsThreads = 160;  // 4 warps of 16 keys, 1 loader
 constexpr int kRowsKeys = 64;      // keys per tile
+// Tiles of 64 keys x 16 rows, over all heads, up to which a prefix goes through
+// rows_kernel.  Measured against attend_kernel, whole calls with caches of 50
+// keys: 12.3 us against 15.4 (8 sequences, 32/8 heads, 64 keys: 16 tiles), 16.4
+// against 17.5 (32 sequences, 256 keys: 256), 10.3 against 16.4 (16, 16/2 heads,
+// d = 64, 1024 keys: 256), 20.6 against 20.5 (32, 32/8 heads, 1024 keys: 1024),
+// 37 against 26.7 (4096 keys: 4096).
+constexpr int kRowsPasses = 1024;
 constexpr int kFinishKeys = 2048;  // keys that a CTA of the weights' part takes at a time
 
 // kLong: 96 KB in flight and two CTAs per SM, the faster stream; else 64 KB and
@@ -81,6 +88,7 @@ struct RowsArgs {
   int nslot;    // partial results per row: the prefix's, then the cache's
   int own_slot; // slot of the cache's first split
   int own_rows; // ceil(G / 16)
+  int pre_rows; // ceil(B G / 16)
   bool direct;  // the only part: write O and lse
   float scale_log2;
   int64_t q_seq;
@@ -108,19 +116,20 @@ __global__ void __launch_bounds__(kRowsThreads, kLong ? 2 : 3)
   launch_dependents();
   // ---- which rows, which keys
   int idx = blockIdx.x, hk, b0, rows, row0, n, split, nsplit, slot, z;
-  const bool pre = idx < a.npre * a.Hkv;
+  const bool pre = idx < a.npre * a.Hkv * a.pre_rows;
   if (pre) {
     hk = idx % a.Hkv;
-    split = idx / a.Hkv;
+    idx /= a.Hkv;
+    row0 = idx % a.pre_rows * 16;
+    split = idx / a.pre_rows;
     nsplit = a.npre;
     b0 = 0;
-    row0 = 0;
     rows = a.B * a.G;
     n = a.P;
     slot = split;
     z = hk;
   } else {
-    idx -= a.npre * a.Hkv;
+    idx -= a.npre * a.Hkv * a.pre_rows;
     hk = idx % a.Hkv;
     idx /= a.Hkv;
     b0 = idx % a.B;
@@ -435,8 +444,9 @@ StepPlan step_plan(const StepArgs& a, bool with_weights) {
   if (n > 64) n = 64;
   p.nown = a.cap == 0 ? 0 : n < 1 ? 1 : (int)n;
   if (a.P > 0) {
-    if (a.B * a.G <= 16) {
-      n = (4 * kSms + a.Hkv - 1) / a.Hkv;
+    const long long pre_rows = ((long long)a.B * a.G + 15) / 16;
+    if (pre_rows == 1 || (a.P + kRowsKeys - 1) / kRowsKeys * pre_rows * a.Hkv <= kRowsPasses) {
+      n = (4 * kSms + a.Hkv * pre_rows - 1) / (a.Hkv * pre_rows);
       if (n > a.P / 256) n = a.P / 256;
       if (n > 64) n = 64;
       p.npre_rows = n < 1 ? 1 : (int)n;
@@ -481,6 +491,7 @@ cudaError_t run_step(const StepArgs& s, const StepPlan& p, cudaStream_t st) {
   a.nslot = p.nown + p.npre_rows + p.npre_tc;
   a.own_slot = p.npre_rows + p.npre_tc;
   a.own_rows = (s.G + 15) / 16;
+  a.pre_rows = (int)(((long long)s.B * s.G + 15) / 16);
   a.direct = p.direct;
   a.scale_log2 = s.scale_log2;
   a.q_seq = s.q_seq;
@@ -516,7 +527,7 @@ cudaError_t run_step(const StepArgs& s, const StepPlan& p, cudaStream_t st) {
     return e != cudaSuccess ? e : run_attend<T, D>(t, tk, tv, st, overlap);
   };
   const long long ctas =
-      (long long)a.npre * a.Hkv + (long long)a.nown * a.Hkv * a.B * a.own_rows;
+      (long long)a.npre * a.Hkv * a.pre_rows + (long long)a.nown * a.Hkv * a.B * a.own_rows;
   if (ctas > 0) {
     CUtensorMap kp, vp, kc, vc;
     // (a map that no CTA uses is a copy of the other)

@@ -233,6 +233,9 @@ STEPS = {
     "long_prefix": (40, 9000, [50 + i for i in range(40)], 100, 8, 2, 64),
     "long_own": (2, 0, [20000, 5001], 20003, 8, 2, 128),
     "long_both": (20, 5000, [3000 - 100 * i for i in range(20)], 3001, 4, 1, 128),
+    "tall_prefix": (70, 4111, [(11 * i) % 33 for i in range(70)], 33, 20, 4, 128),
+    "crowded": (130, 3001, [(7 * i) % 21 for i in range(130)], 21, 16, 8, 64),
+    "many_long": (150, 3, [5001 - 33 * i for i in range(150)], 5001, 4, 2, 64),
 }
 
 
