@@ -90,6 +90,7 @@ __global__ void __launch_bounds__(kKwThreads, 1)
   const int z = blockIdx.x / a.Hkv % a.nsplit;
   const int t_glob = blockIdx.x / a.Hkv / a.nsplit;
 
+  launch_dependents();
   if (warp == 0) {
     const SeqPair p = find_pair(a.cu_k, a.cu_q, a.nseq, 1, t_glob);
     if (lane == 0) *reinterpret_cast<SeqPair*>(work) = p;
@@ -320,6 +321,7 @@ __global__ void __launch_bounds__(256) add_parts_kernel(KwArgs a) {
       hi = mid;
   }
   if (j < a.cu_k[lo] || j >= a.cu_k[lo + 1]) return;
+  wait_prior_grids();  // key_weights_kernel's parts
   float s = 0.f;
   for (int z = 0; z < a.nsplit; ++z) s += a.parts[z * n + at];
   a.weights[at] += s;
@@ -383,8 +385,7 @@ cudaError_t launch_key_weights(const PromptArgs& p, cudaStream_t s) {
   else
     e = p.d == 128 ? run_key_weights<__half, 128>(a, tq, s) : run_key_weights<__half, 64>(a, tq, s);
   if (e != cudaSuccess || a.nsplit == 1) return e;
-  add_parts_kernel<<<(unsigned)(((size_t)a.Hkv * a.Tk + 255) / 256), 256, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_after(add_parts_kernel, dim3((unsigned)(((size_t)a.Hkv * a.Tk + 255) / 256)), 256, 0, true, s, a);
 }
 
 }  // namespace ig

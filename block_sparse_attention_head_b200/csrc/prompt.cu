@@ -695,6 +695,7 @@ __global__ void __launch_bounds__(128) combine_kernel(TcArgs a) {
     }
     if (tok >= a.cu_q[lo + 1]) return;
   }
+  wait_prior_grids();  // attend_kernel's parts
   float top = -INFINITY;
   for (int z = 0; z < a.nsplit; ++z) top = fmaxf(top, a.lse_part[z * rows + row]);
   float o[D / 32], sum = 0.f;
@@ -816,19 +817,12 @@ cudaError_t launch_prompt_attention(const PromptArgs& p, cudaStream_t s) {
     e = make_tmap_rows(&tv, p.Tk ? p.V : p.Q, p.dtype, p.d, p.Tk ? p.Tk : 1, p.Hkv, p.v_tok, p.v_head);
   if (e == cudaSuccess) e = dispatch_attend(a, p.dtype, p.d, tk, tv, s);
   if (e != cudaSuccess || !a.partial) return e;
-  const unsigned grid = (unsigned)(((long long)p.Tq * p.Hq + 3) / 4);
-  if (p.dtype == IG_BF16) {
-    if (p.d == 128)
-      combine_kernel<__nv_bfloat16, 128><<<grid, 128, 0, s>>>(a);
-    else
-      combine_kernel<__nv_bfloat16, 64><<<grid, 128, 0, s>>>(a);
-  } else {
-    if (p.d == 128)
-      combine_kernel<__half, 128><<<grid, 128, 0, s>>>(a);
-    else
-      combine_kernel<__half, 64><<<grid, 128, 0, s>>>(a);
-  }
-  return cudaGetLastError();
+  const dim3 grid((unsigned)(((long long)p.Tq * p.Hq + 3) / 4));
+  if (p.dtype == IG_BF16)
+    return p.d == 128 ? launch_after(combine_kernel<__nv_bfloat16, 128>, grid, 128, 0, true, s, a)
+                      : launch_after(combine_kernel<__nv_bfloat16, 64>, grid, 128, 0, true, s, a);
+  return p.d == 128 ? launch_after(combine_kernel<__half, 128>, grid, 128, 0, true, s, a)
+                    : launch_after(combine_kernel<__half, 64>, grid, 128, 0, true, s, a);
 }
 
 }  // namespace ig
