@@ -10,15 +10,22 @@
 //   P_t = 2^(c S_t - m_t), rounded to the tensors' type, into S_t's columns
 //   O_t += P_t V_j      tcgen05 with A (P_t) read from TMEM
 // with c = softmax_scale log2(e) and m_t the running maximum, raised only when
-// it grows by more than 8 (P <= 256), which keeps rescaling O rare.  The two
-// chains run independently (two softmax warpgroups, one thread per row; two MMA
-// warps), so one chain's exponentials overlap the other's MMAs.  A CTA with one
+// it grows by more than 8 (P <= 256), which keeps rescaling O rare.  Each chain
+// has a softmax warpgroup (one thread per row) and an MMA warp; K and V have a
+// loader warp each.  The chains take turns on the tensor pipe, so that one's
+// exponentials run under the other's products: left to themselves they fall
+// into step, and a key tile takes 4180 cycles instead of 3120.  A CTA with one
 // row tile gives chain 0 the even and chain 1 the odd key tiles and merges the
 // two partial softmaxes at the end.
 //
 // Bound: 4 * 512 tensor cycles per key tile and CTA (d = 128) against 2 * 1024
-// of exponentials on the MUFU; a quarter of the exponentials of unmasked tiles
-// are therefore evaluated on the FMA pipe.
+// of exponentials on the MUFU, a quarter of which (in unmasked tiles) run on
+// the FMA pipe instead.  16384 tokens, 16/4 heads, d = 128: 0.90 ms in a single
+// run (1.23 PFLOP/s, tensor pipe 63%), 0.97-1.0 back to back, where the card
+// is at its power limit.  Short sequences: one
+// wave of 148 CTAs of 256 rows takes 14.9 us on one key tile (launch, ends,
+// query rows, first product; output, exit), 28.9 on 8 and 44.4 on 16, that is
+// 1.8 to 1.9 us per key tile.
 //
 // Few rows, many keys: nsplit CTAs share a row tile pair, each over its part
 // of the key tiles, and write normalised partial outputs with their log-sum-
@@ -743,6 +750,10 @@ static long long row_pairs_one(int n, int G) { return ((long long)n * G + 255) >
 
 // CTAs per row tile pair: where the pairs leave SMs idle, the keys are split
 // so that about every SM has a CTA, in parts of at least 4 key tiles.
+// Measured (graph replays, bf16, d = 128), parts of at least 2, 4, 8, 16, 32
+// tiles: 64 rows of 8/2 heads on 8192 keys 22.8, 21.3, 25.9, 38.1, 64.3 us; on
+// 32768 keys 32.8, 32.9, 32.3, 41.4, 65.5; a step of 32 sequences, 32/8 heads,
+// behind 4000 keys 26.2, 22.9, 28.7, 48.0, 48.0.
 static int key_splits(long long ctas, long long keys) {
   if (ctas >= kSms) return 1;
   const long long by_keys = keys / 512;
