@@ -310,6 +310,8 @@ __global__ void __launch_bounds__(kKwThreads, 1)
 // weights += the parts' sums, for the keys of sequences (one thread each).
 __global__ void __launch_bounds__(256) add_parts_kernel(KwArgs a) {
   const size_t n = (size_t)a.Hkv * a.Tk, at = (size_t)blockIdx.x * 256 + threadIdx.x;
+  // this grid's end is that of key_weights_kernel's, even where no key is joined
+  if (blockIdx.x == 0) wait_prior_grids();
   if (at >= n) return;
   const int j = (int)(at % a.Tk);
   int lo = 0, hi = a.nseq;  // the last sequence that starts at or before j

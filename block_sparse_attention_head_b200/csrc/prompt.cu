@@ -687,6 +687,8 @@ __global__ void __launch_bounds__(128) combine_kernel(TcArgs a) {
   const int lane = threadIdx.x & 31;
   const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   const size_t rows = (size_t)a.Tq * a.Hq;
+  // this grid's end is that of attend_kernel's, even where no row is joined
+  if (blockIdx.x == 0) wait_prior_grids();
   if (row >= (long long)rows) return;
   const int tok = (int)(row / a.Hq), head = (int)(row % a.Hq);
   if (a.cu_q) {  // rows of no sequence stay as they were

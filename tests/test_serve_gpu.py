@@ -207,6 +207,35 @@ def test_prompt_no_queries_or_no_keys_at_all():
     ig.device_status()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_split_keys_without_any_sequence_then_a_call_with_new_ends(d):
+    """No row and no key in a sequence where the keys are split over CTAs:
+    nothing is written, and the ends and the workspace may change right behind."""
+    Tq, Tk, Hq, Hkv = 700, 9000, 4, 2
+    q, k, v = normal(1, Tq, Hq, d), normal(2, Tk, Hkv, d), normal(3, Tk, Hkv, d)
+    ends_q, ends_k = cu([Tq]), cu([Tk])
+    want, want_lse = ig.prompt_attention(q, k, v, ends_q, ends_k)
+    want_w = ig.key_weights(q, k, want_lse, ends_q, ends_k, torch.zeros(Hkv, Tk, device="cuda"))
+    work = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    cu_q, cu_k = cu([0]), cu([0])
+    out = torch.full((Tq, Hq, d), 7.0, dtype=BF, device="cuda")
+    lse = torch.full((Hq, Tq), 7.0, device="cuda")
+    w = torch.full((Hkv, Tk), 2.0, device="cuda")
+    for _ in range(20):
+        ig.prompt_attention(q, k, v, cu_q, cu_k, out=out, lse=lse, workspace=work)
+        cu_q.copy_(ends_q), cu_k.copy_(ends_k), work.fill_(255)
+        cu_q.zero_(), cu_k.zero_()
+        ig.key_weights(q, k, lse, cu_q, cu_k, w, workspace=work)
+        cu_q.copy_(ends_q), cu_k.copy_(ends_k), work.fill_(255)
+        cu_q.zero_(), cu_k.zero_()
+    assert (out == 7).all() and (lse == 7).all() and (w == 2).all()
+    cu_q.copy_(ends_q), cu_k.copy_(ends_k)
+    ig.prompt_attention(q, k, v, cu_q, cu_k, out=out, lse=lse, workspace=work)
+    ig.key_weights(q, k, lse, cu_q, cu_k, w.zero_(), workspace=work)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse) and torch.equal(w, want_w)
+    ig.device_status()
+
+
 def test_prompt_bad_ends_are_reported_and_stay_in_range():
     q, k = normal(1, 20, 2, 64), normal(2, 20, 2, 64)
     bad = torch.tensor([0, 500], dtype=torch.int32, device="cuda")
