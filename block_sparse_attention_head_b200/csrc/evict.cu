@@ -373,8 +373,10 @@ size_t evict_ws(int B, int Hkv, int budget) {
 template <bool kHeld>
 static cudaError_t run_select(const EvictArgs& a, int S, int threads, size_t smem, cudaStream_t s) {
   if (smem > 40 * 1024) {  // 48 KB with the static part need no leave
-    const cudaError_t e =
-        cudaFuncSetAttribute(evict_select_kernel<kHeld>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // the most that any call asks for: the limit is the kernel's, and another
+    // thread's call may be between setting it and its launch
+    const cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<kHeld>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kEvictKeys * 4);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchAttribute attr{};

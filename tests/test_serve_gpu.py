@@ -13,6 +13,7 @@ half a step of the 16-bit type (2^-8 bf16, 2^-11 fp16),
             of the sum for adding it up in fp32
 """
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -538,6 +539,42 @@ def test_two_streams_at_once_and_again_the_same_bits():
         torch.cuda.synchronize()
         for g, w in zip(got, want):
             assert all(torch.equal(torch.nan_to_num(a.float()), torch.nan_to_num(b.float())) for a, b in zip(g, w))
+    ig.device_status()
+
+
+def test_evict_from_four_threads_with_caches_of_different_size():
+    """Host threads with a stream and a workspace each, whose calls ask for
+    different amounts of shared memory (150 caches: no cluster)."""
+    B, Hkv, d, times = 75, 2, 64, 2000
+    L, stores, errors, start = ig.lib(), [], [], threading.Barrier(4)
+    for cap in (12000, 20000, 30000, 40000):
+        t = [torch.zeros(B, Hkv, cap, d, dtype=BF, device="cuda"), torch.zeros(B, Hkv, cap, d, dtype=BF, device="cuda"),
+             torch.rand(B, Hkv, cap, device="cuda"),
+             torch.arange(cap, dtype=torch.int32, device="cuda").expand(B, Hkv, cap).contiguous(),
+             torch.full((B,), 40, dtype=torch.int32, device="cuda")]
+        t[0][:, :, :40], t[1][:, :, :40] = normal(1, B, Hkv, 40, d), normal(2, B, Hkv, 40, d)
+        before = [x[:, :, :40].clone() if x.dim() > 1 else x.clone() for x in t]
+        stores.append((t, before, torch.empty(1 << 20, dtype=torch.uint8, device="cuda"), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+
+    def work(t, _, ws, stream):  # (the C entry, so that the threads meet inside it and not at the interpreter's lock)
+        p = bytes(ig.CacheParams(B, Hkv, Hkv, d, 0, t[0].shape[2], 0, 1.0, Hkv * d, 0))
+        at = [x.data_ptr() for x in t]
+        start.wait()
+        for _ in range(times):
+            rc = L.instagen_evict(*at, p, 30, 5, *at, t[0].shape[2], ws.data_ptr(), ws.numel(), stream.cuda_stream)
+            if rc:
+                errors.append((t[0].shape[2], rc))
+
+    threads = [threading.Thread(target=work, args=s) for s in stores]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    for t, before, _, _ in stores:  # (from the second call on there is nothing to evict)
+        check_evict(before, [x[:, :, :40] if x.dim() > 1 else x for x in t], 30, 5)
     ig.device_status()
 
 
