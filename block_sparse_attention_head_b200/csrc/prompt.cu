@@ -783,6 +783,7 @@ static cudaError_t dispatch_attend(const TcArgs& a, int dtype, int d, const CUte
 }
 
 static int prompt_splits(const PromptArgs& a) {
+  if (a.Tq == 0) return 1;  // nothing to join
   return key_splits(row_pairs(a.Tq, a.G, a.nseq) * a.Hkv, a.Tk / a.nseq);
 }
 

@@ -162,3 +162,11 @@ def test_binding_refuses_cpu_tensors(lib):
             call()
     with pytest.raises(TypeError):
         ig.prompt_attention(None, k, k, c, c)
+
+
+@pytest.mark.parametrize("kw", [dict(Tq=0), dict(Tk=0), dict(Tq=0, Tk=0), dict()])
+@pytest.mark.parametrize("Tk", [1, 4096, 100000])
+def test_every_valid_prompt_has_a_workspace_size(lib, Tk, kw):
+    p = prompt(nseq=1, Hq=8, Hkv=8, **{"Tk": Tk, "Tq": 4, **kw})
+    assert lib.instagen_prompt_attention_workspace_size(ctypes.byref(p)) >= 256
+    assert lib.instagen_key_weights_workspace_size(ctypes.byref(p)) >= 256

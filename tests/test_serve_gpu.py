@@ -578,6 +578,16 @@ def test_evict_from_four_threads_with_caches_of_different_size():
     ig.device_status()
 
 
+@pytest.mark.parametrize("Tk", [700, 4096, 100000])
+def test_no_queries_before_many_keys(Tk):
+    q, k = normal(1, 0, 8, 64), normal(2, Tk, 8, 64)
+    O, lse = ig.prompt_attention(q, k, k, cu([0]), cu([Tk]))
+    assert O.shape == (0, 8, 64) and lse.shape == (8, 0)
+    w = ig.key_weights(q, k, lse, cu([0]), cu([Tk]), torch.full((8, Tk), 2.0, device="cuda"))
+    assert (w == 2).all()
+    ig.device_status()
+
+
 # ----------------------------------------------------------------- refusals
 def test_binding_refusals():
     q, k = normal(1, 8, 4, 64), normal(2, 8, 2, 64)
