@@ -84,30 +84,41 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 
-// 2^x of two values on the FMA pipe: x = n + f with n the nearest integer
-// (adding 1.5 * 2^23 leaves n in the low mantissa bits) and 2^f, |f| <= 1/2, by
-// the degree-4 or degree-5 polynomial with the smallest relative error (2.6e-6
-// and 1.6e-7; Remez exchange, coefficients rounded to fp32); n is added to the
-// exponent.  x below -126 gives 2^-126.
+// 2^x of two values on the FMA pipe, x < 128: x = n + f with n the nearest
+// integer (adding 1.5 * 2^23 leaves n in the low mantissa bits) and 2^f, |f| <=
+// 1/2, by a polynomial with the smallest relative error (Remez exchange,
+// coefficients rounded to fp32).
+//   Degree 5 (1.6e-7): times 2^n, which has the bits 0 for n = -127, so below
+//   2^-126.5 gives 0, and NaN stays NaN.
+//   Degree 4 (2.9e-6, 2.6e-6 without the constant held at 1): n is added to the
+//   exponent's bits.  x is at least -127, where f >= 0 and the constant's bits
+//   end at 0 or above: below 2^-126 gives less, -inf gives 0.  A NaN does not
+//   stay one (as a product it would: the 16384-token prompt takes 2% longer);
+//   the caller's row maximum keeps it.
 template <int kDegree>
 __device__ __forceinline__ uint64_t ex2_poly2(uint64_t x2) {
-  constexpr float c0 = kDegree == 5 ? 1.0000001192092896f : 0.9999992847442627f;
-  constexpr float c1 = kDegree == 5 ? 0.6931469440460205f : 0.6931217908859253f;
-  constexpr float c2 = kDegree == 5 ? 0.24022120237350464f : 0.240247443318367f;
-  constexpr float c3 = kDegree == 5 ? 0.05550713092088699f : 0.05591785907745361f;
-  constexpr float c4 = kDegree == 5 ? 0.009675540961325169f : 0.009570102207362652f;
+  constexpr float c0 = kDegree == 5 ? 1.0000001192092896f : 1.f;
+  constexpr float c1 = kDegree == 5 ? 0.6931469440460205f : 0.6931241750717163f;
+  constexpr float c2 = kDegree == 5 ? 0.24022120237350464f : 0.24024099111557007f;
+  constexpr float c3 = kDegree == 5 ? 0.05550713092088699f : 0.055906426161527634f;
+  constexpr float c4 = kDegree == 5 ? 0.009675540961325169f : 0.009582852944731712f;
   constexpr float c5 = 0.0013276472454890609f;
   static_assert(kDegree == 4 || kDegree == 5, "degree");
   float a, b;
   unpack2(x2, a, b);
-  asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(a));  // -126
-  asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(b));
+  asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(a));  // -127
+  asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(b));
   const uint64_t x = pack2(a, b);
   const uint64_t n = add2(x, pack2(12582912.f, 12582912.f));
   const uint64_t f = fma2(add2(n, pack2(-12582912.f, -12582912.f)), pack2(-1.f, -1.f), x);
@@ -117,11 +128,13 @@ __device__ __forceinline__ uint64_t ex2_poly2(uint64_t x2) {
   p = fma2(p, f, pack2(c2, c2));
   p = fma2(p, f, pack2(c1, c1));
   p = fma2(p, f, pack2(c0, c0));
-  float n0, n1, p0, p1;
+  float n0, n1;
   unpack2(n, n0, n1);
+  const uint32_t e0 = __float_as_uint(n0) << 23, e1 = __float_as_uint(n1) << 23;
+  if constexpr (kDegree == 5) return mul2(p, pack2(__uint_as_float(e0 + 0x3f800000u), __uint_as_float(e1 + 0x3f800000u)));
+  float p0, p1;
   unpack2(p, p0, p1);
-  return pack2(__uint_as_float(__float_as_uint(p0) + (__float_as_uint(n0) << 23)),
-               __uint_as_float(__float_as_uint(p1) + (__float_as_uint(n1) << 23)));
+  return pack2(__uint_as_float(__float_as_uint(p0) + e0), __uint_as_float(__float_as_uint(p1) + e1));
 }
 
 template <typename T>
@@ -491,9 +504,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
       for (int c = 0; c < 128; c += 2)
-        mx[(c >> 1) & 3] = fmax3(mx[(c >> 1) & 3], x4[c >> 5][c & 31], x4[c >> 5][(c & 31) + 1]);
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
-      const bool raise = top > m + kTcThreshold;  // the first key of a row always raises
+        mx[(c >> 1) & 3] = fmax3_nan(mx[(c >> 1) & 3], x4[c >> 5][c & 31], x4[c >> 5][(c & 31) + 1]);
+      const float top = fmax3_nan(fmax3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]) * a.scale_log2;
+      // the first key of a row always raises; NaN does, and l is NaN from there on
+      const bool raise = !(top <= m + kTcThreshold);
       float alpha = 1.f;
       if (raise) {
         alpha = ex2_approx(m - top);

@@ -363,8 +363,9 @@ int instagen_forward_layout_get(const instagen_params* p, instagen_forward_layou
  * in place).  Contents of K and V rows behind a sequence's end (or past a cache's length)
  * never matter, NaN included; values a sequence's own rows hold must be
  * finite (a non-finite V row may reach earlier rows of the same sequence
- * through a zero probability).  Results do not depend on timing: no atomics
- * on floats.  Pointers to 16-bit tensors, O and lse must be 16-byte aligned.
+ * through a zero probability).  A logit of -inf (dots may overflow) weighs 0;
+ * a weight below 2^-126 of its row's largest may count as less, down to 0.
+ * Results do not depend on timing: no atomics on floats.  Pointers to 16-bit tensors, O and lse must be 16-byte aligned.
  * Workspaces are scratch: 256-byte aligned, no contents kept; calls that may
  * overlap on the GPU (two streams, two captured graphs) need one each.  A
  * size function returns 0 for invalid parameters and at least 256 otherwise;

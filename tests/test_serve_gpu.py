@@ -588,6 +588,90 @@ def test_no_queries_before_many_keys(Tk):
     ig.device_status()
 
 
+# --------------------------------------------------- logits that are not finite
+def nan_rows(got, bad, what):
+    """Rows [..., rows] (or rows with a last dimension) that are NaN: exactly those of bad."""
+    assert torch.equal(torch.isnan(got.float()), bad), what
+
+
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("nq", [100, 300])  # one row tile, two
+def test_a_nan_key_shows_in_every_row_that_sees_it(nq, dtype):
+    nk, Hq, Hkv, d = 640, 2, 1, 64
+    q, k, v = normal(1, nq, Hq, d, dtype=dtype), normal(2, nk, Hkv, d, dtype=dtype), normal(3, nk, Hkv, d, dtype=dtype)
+    for key in (0, 5, 6, 7, 134, 255, 262, 390):  # in tiles without a mask
+        x = k.clone()
+        x[key, 0, 3] = math.nan
+        O, lse = ig.prompt_attention(q, x, v, cu([nq]), cu([nk]), causal=False)
+        assert torch.isnan(O).all() and torch.isnan(lse).all(), key
+        # causal with as many keys as queries: the rows before do not see it
+        O, lse = ig.prompt_attention(q, x[:nq], v[:nq], cu([nq]), cu([nq]))
+        want = torch.arange(nq, device="cuda") >= key
+        nan_rows(lse, want.expand(Hq, nq), key)
+        nan_rows(O, want[:, None, None].expand(nq, Hq, d), key)
+    ig.device_status()
+
+
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+def test_a_nan_query_shows_in_the_weights_of_the_keys_it_sees(dtype):
+    nq, nk, d = 300, 700, 64
+    q, k = normal(1, nq, 1, d, dtype=dtype), normal(2, nk, 1, d, dtype=dtype)
+    _, lse = ig.prompt_attention(q, k, k, cu([nq]), cu([nk]))
+    for row in (0, 1, 2, 3, 130, 137, 299):
+        x = q.clone()
+        x[row, 0, 5] = math.nan
+        w = ig.key_weights(x, k, lse, cu([nq]), cu([nk]), torch.zeros(1, nk, device="cuda"))
+        nan_rows(w[0], torch.arange(nk, device="cuda") <= row + nk - nq, row)
+
+
+def test_rows_without_lse_add_nothing_to_the_weights():
+    """lse = -inf: rows that a caller leaves out, here in tiles without a mask."""
+    nq, nk, Hq, Hkv, d = 300, 900, 4, 2, 128
+    q, k = normal(1, nq, Hq, d), normal(2, nk, Hkv, d)
+    _, lse = ig.prompt_attention(q, k, k, cu([nq]), cu([nk]))
+    none = torch.full_like(lse, -math.inf)
+    w = ig.key_weights(q, k, none, cu([nq]), cu([nk]), torch.zeros(Hkv, nk, device="cuda"))
+    assert (w == 0).all()
+    some = lse.clone()
+    some[:, 50:] = -math.inf
+    w = ig.key_weights(q, k, some, cu([nq]), cu([nk]), torch.zeros(Hkv, nk, device="cuda"), causal=False)
+    want = ig.key_weights(q[:50], k, lse[:, :50].contiguous(), cu([50]), cu([nk]), torch.zeros(Hkv, nk, device="cuda"),
+                          causal=False)
+    within(w, want.double(), 200 * 2.0 ** -23 * want.double(), "weights")  # the same terms, added in another order
+
+
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("nq", [100, 300])
+def test_logits_of_minus_infinity_weigh_nothing(nq, dtype):
+    """Keys whose every logit is -inf are as keys that are not there, whatever
+    their values; rows with no other logit are as rows that see no key."""
+    nk, d = 384, 64
+    q, k, v = normal(1, nq, 1, d, dtype=dtype), normal(2, nk, 1, d, dtype=dtype), normal(3, nk, 1, d, dtype=dtype)
+    q[..., 0] = q[..., 0].abs() + 1
+    far = torch.arange(nk, device="cuda") % 16 >= 6
+    k[far, :, 0] = -math.inf
+    v[far] = 60000.0 if dtype == FP else 3e38
+    O, lse = ig.prompt_attention(q, k, v, cu([nq]), cu([nk]), causal=False)
+    near = ~far
+    o, l, _, tol, tol_l, _ = attend(q[:, 0], k[near, 0], v[near, 0], d ** -0.5)
+    within(O[:, 0], o, tol, "O")
+    within(lse[0], l, tol_l, "lse")
+    k[..., 0] = -math.inf
+    O, lse = ig.prompt_attention(q, k, v, cu([nq]), cu([nk]), causal=False)
+    assert (O == 0).all() and (lse == -math.inf).all()
+    w = ig.key_weights(q, k, torch.zeros_like(lse), cu([nq]), cu([nk]), torch.zeros(1, nk, device="cuda"), causal=False)
+    assert (w == 0).all()
+
+
+def test_logits_far_below_the_largest_weigh_what_they_should():
+    # weights of 2^-187 times values of 3e38 are nothing; 2^-126 of them would be 3.5
+    nq, nk, d = 256, 256, 64
+    q, k, v = torch.zeros(nq, 1, d, dtype=BF, device="cuda"), torch.zeros(nk, 1, d, dtype=BF, device="cuda"), normal(3, nk, 1, d)
+    q[..., 0], k[1:, 0, 0], v[1:] = 1.0, -130.0, 3e38
+    O, lse = ig.prompt_attention(q, k, v, cu([nq]), cu([nk]), causal=False, softmax_scale=1.0)
+    assert torch.equal(O, v[:1].expand(nq, 1, d)) and (lse == 0).all()
+
+
 # ----------------------------------------------------------------- refusals
 def test_binding_refusals():
     q, k = normal(1, 8, 4, 64), normal(2, 8, 2, 64)
