@@ -318,7 +318,10 @@ __global__ void __launch_bounds__(kRowsThreads, kLong ? 2 : 3)
 #pragma unroll
     for (int w = 0; w < 4; ++w) top = fmaxf(top, ml[16 * w + r]);
 #pragma unroll
-    for (int w = 0; w < 4; ++w) sum += top == -INFINITY ? 0.f : ml[64 + 16 * w + r] * ex2_approx(ml[16 * w + r] - top);
+    for (int w = 0; w < 4; ++w) {
+      const float mw = ml[16 * w + r], lw = ml[64 + 16 * w + r];
+      sum += mw == -INFINITY ? lw : lw * ex2_approx(mw - top);  // (no maximum: 0, or NaN)
+    }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -363,8 +366,10 @@ __global__ void __launch_bounds__(256) finish_kernel(RowsArgs a) {
     for (int i = lane + 32; i < a.nslot; i += 32) top = fmaxf(top, lp[i * rows]);
 #pragma unroll
     for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    sum = top == -INFINITY ? 0.f : exp2f(x0 - top);
-    for (int i = lane + 32; i < a.nslot; i += 32) sum += top == -INFINITY ? 0.f : exp2f(lp[i * rows] - top);
+    // (top does not keep a NaN, the sum does)
+    auto part = [&](float x) { return x == -INFINITY ? 0.f : exp2f(x - top); };
+    sum = part(x0);
+    for (int i = lane + 32; i < a.nslot; i += 32) sum += part(lp[i * rows]);
     sum = warp_sum(sum);
     const float y = sum == 0.f ? -INFINITY : top + log2f(sum);
     if (lane == 0) lse2[g] = y;

@@ -363,7 +363,8 @@ int instagen_forward_layout_get(const instagen_params* p, instagen_forward_layou
  * in place).  Contents of K and V rows behind a sequence's end (or past a cache's length)
  * never matter, NaN included; values a sequence's own rows hold must be
  * finite (a non-finite V row may reach earlier rows of the same sequence
- * through a zero probability).  A logit of -inf (dots may overflow) weighs 0;
+ * through a zero probability).  A NaN in Q or K still shows: O and lse of every
+ * row with a NaN logit are NaN.  A logit of -inf (dots may overflow) weighs 0;
  * a weight below 2^-126 of its row's largest may count as less, down to 0.
  * Results do not depend on timing: no atomics on floats.  Pointers to 16-bit tensors, O and lse must be 16-byte aligned.
  * Workspaces are scratch: 256-byte aligned, no contents kept; calls that may

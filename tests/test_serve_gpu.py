@@ -672,6 +672,26 @@ def test_logits_far_below_the_largest_weigh_what_they_should():
     assert torch.equal(O, v[:1].expand(nq, 1, d)) and (lse == 0).all()
 
 
+@pytest.mark.parametrize("keep", [False, True], ids=["plain", "weights"])
+@pytest.mark.parametrize("P,cap", [(0, 70), (70, 0), (1, 1), (3000, 5), (3000, 3000), (30000, 5)])
+def test_a_nan_query_shows_in_its_step(P, cap, keep):
+    """Every logit of the row is NaN, in whichever part its keys are."""
+    B, Hq, Hkv, d = 40, 4, 2, 64
+    q, kp, kc = normal(1, B, Hq, d), normal(2, Hkv, P, d), normal(4, B, Hkv, cap, d)
+    lens = torch.full((B,), cap, dtype=torch.int32, device="cuda")
+    q[3, 1, 7] = math.nan
+    w = torch.zeros(B, Hkv, cap, device="cuda") if keep else None
+    O, lse = ig.prefix_attention(q, kp, kp, kc, kc, lens, weights=w)
+    bad = torch.zeros(B, Hq, dtype=torch.bool, device="cuda")
+    bad[3, 1] = True
+    nan_rows(lse, bad, "lse")
+    nan_rows(O, bad[..., None].expand(B, Hq, d), "O")
+    if keep:
+        bad = torch.zeros(B, Hkv, cap, dtype=torch.bool, device="cuda")
+        bad[3, 0] = True
+        nan_rows(w, bad, "weights")
+
+
 # ----------------------------------------------------------------- refusals
 def test_binding_refusals():
     q, k = normal(1, 8, 4, 64), normal(2, 8, 2, 64)
