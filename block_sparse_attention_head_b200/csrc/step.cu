@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(256) finish_kernel(RowsArgs a) {
     for (int i = lane + 32; i < a.nslot; i += 32) sum += part(lp[i * rows]);
     sum = warp_sum(sum);
     const float y = sum == 0.f ? -INFINITY : top + log2f(sum);
-    if (lane == 0) lse2[g] = y;
+    if (lane == 0) lse2[g] = y == -INFINITY ? INFINITY : y;  // scores of -inf alone: no weight
     if (!join) continue;
     if (lane == 0 && a.lse) a.lse[row0 + g] = y * kLn2;
     float o[D / 32];

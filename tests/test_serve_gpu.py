@@ -692,6 +692,17 @@ def test_a_nan_query_shows_in_its_step(P, cap, keep):
         nan_rows(w, bad, "weights")
 
 
+@pytest.mark.parametrize("P", [0, 100])
+def test_a_step_whose_logits_are_all_minus_infinity_adds_no_weight(P):
+    B, Hq, Hkv, d, cap = 3, 4, 2, 64, 90
+    q, kp, kc = normal(1, B, Hq, d).abs() + 1, normal(2, Hkv, P, d), normal(4, B, Hkv, cap, d)
+    kp[..., 0], kc[..., 0] = -math.inf, -math.inf
+    lens = torch.tensor([90, 33, 0], dtype=torch.int32, device="cuda")
+    w = torch.full((B, Hkv, cap), 2.0, device="cuda")
+    O, lse = ig.prefix_attention(q, kp, kp.abs().nan_to_num(posinf=1), kc, kc.abs().nan_to_num(posinf=1), lens, weights=w)
+    assert (O == 0).all() and (lse == -math.inf).all() and (w == 2).all()
+
+
 # ----------------------------------------------------------------- refusals
 def test_binding_refusals():
     q, k = normal(1, 8, 4, 64), normal(2, 8, 2, 64)
