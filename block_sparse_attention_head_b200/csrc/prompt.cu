@@ -10,7 +10,10 @@
 //   P_t = 2^(c S_t - m_t), rounded to the tensors' type, into S_t's columns
 //   O_t += P_t V_j      tcgen05 with A (P_t) read from TMEM
 // with c = softmax_scale log2(e) and m_t the running maximum, raised only when
-// it grows by more than 8 (P <= 256), which keeps rescaling O rare.  Each chain
+// it grows by more than 8 (P <= 256), which keeps rescaling O rare.  For fp16,
+// whose steps are 2^-24 from 2^-14 down, m_t is held 7 lower (P <= 2^15): a weight
+// of 2^-21 of the row's largest still has all its digits, a smaller one is off by
+// at most 2^-32 of it (without: 2^-14 and 2^-25, which l would not share).  Each chain
 // has a softmax warpgroup (one thread per row) and an MMA warp; K and V have a
 // loader warp each.  The chains take turns on the tensor pipe, so that one's
 // exponentials run under the other's products: left to themselves they fall
@@ -45,6 +48,7 @@ namespace {
 constexpr int kTcThreads = 384;
 constexpr int kTcRows = 256;        // query rows per CTA
 constexpr float kTcThreshold = 8.f;
+constexpr float kTcHalfShift = 7.f;  // fp16: m below the row's maximum
 // TMEM columns: S_0 [0,128), S_1 [128,256), O_0 [256,..), O_1 [384,..)
 constexpr uint32_t kTcO = 256;
 
@@ -205,6 +209,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     attend_kernel(TcArgs a, const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v) {
   using L = TcSmem<D>;
   constexpr bool kHalf = std::is_same<T, __half>::value;
+  constexpr float kShift = kHalf ? kTcHalfShift : 0.f;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* xch = reinterpret_cast<float*>(smem + L::kXch);
@@ -505,7 +510,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
       for (int c = 0; c < 128; c += 2)
         mx[(c >> 1) & 3] = fmax3_nan(mx[(c >> 1) & 3], x4[c >> 5][c & 31], x4[c >> 5][(c & 31) + 1]);
-      const float top = fmax3_nan(fmax3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]) * a.scale_log2;
+      const float top = fmax3_nan(fmax3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]) * a.scale_log2 - kShift;
       // the first key of a row always raises; NaN does, and l is NaN from there on
       const bool raise = !(top <= m + kTcThreshold);
       float alpha = 1.f;

@@ -105,6 +105,8 @@ __global__ void __launch_bounds__(kRowsThreads, kLong ? 2 : 3)
     rows_kernel(RowsArgs a, const __grid_constant__ CUtensorMap tmap_kp, const __grid_constant__ CUtensorMap tmap_vp,
                 const __grid_constant__ CUtensorMap tmap_kc, const __grid_constant__ CUtensorMap tmap_vc) {
   using L = RowsSmem<D, kLong>;
+  // fp16: the largest weight is 2^15, so that small ones keep their digits (see prompt.cu)
+  constexpr float kShift = std::is_same<T, __half>::value ? 15.f : 0.f;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* ml = reinterpret_cast<float*>(smem + L::kMl);
@@ -246,7 +248,7 @@ __global__ void __launch_bounds__(kRowsThreads, kLong ? 2 : 3)
       float top = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const float mn = fmaxf(m[h], top);
+      const float mn = fmaxf(m[h], top - kShift);
       const float base = mn == -INFINITY ? 0.f : mn;  // no key so far
       alpha[h] = ex2_approx(m[h] - base);
       moved |= mn > m[h];

@@ -357,7 +357,8 @@ int instagen_forward_layout_get(const instagen_params* p, instagen_forward_layou
  * Shared by these entry points: 16-bit tensors are all bf16 or all fp16
  * (dtype); dots and softmax statistics are fp32; the probabilities that
  * multiply V are rounded to the tensors' type (each rounding at most half a
- * step of it), O once at the end; lse is the natural log of the sum of
+ * step of it, and for fp16 below 2^-21 of the row's largest at most 2^-32 of
+ * that), O once at the end; lse is the natural log of the sum of
  * exp(softmax_scale * q.k) and -inf for a row that sees no key, whose O is 0.
  * Outputs must not overlap inputs (weights is both, and so are evict's tensors
  * in place).  Contents of K and V rows behind a sequence's end (or past a cache's length)

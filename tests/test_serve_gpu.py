@@ -703,6 +703,47 @@ def test_a_step_whose_logits_are_all_minus_infinity_adds_no_weight(P):
     assert (O == 0).all() and (lse == -math.inf).all() and (w == 2).all()
 
 
+# Keys whose weights are small beside the largest: fp16's steps are 2^-24 from
+# 2^-14 down, so the weights are multiplied into its range before they are
+# rounded.  The largest is at least 2^7 there, so that a weight is off by at
+# most half a step or by 2^-25 / 2^7 of the largest: no more than
+#   u |O| + (u + 2 |dx| + 2^-19) sum_j p_j |v_j| + 2^-32 max_j p_j sum_j |v_j|.
+def tail_check(O, x, v, dx):
+    p = torch.softmax(x, -1)
+    o, u = p @ v, 2.0 ** -11
+    tol = u * o.abs() + (u + 2 * dx[:, None] + 2.0 ** -19) * (p @ v.abs()) + 2.0 ** -32 * v.abs().sum(0)
+    within(O, o, tol, "O")
+
+
+@pytest.mark.parametrize("sink", [0, 999, 3999])
+@pytest.mark.parametrize("nq", [60, 250])
+def test_fp16_small_weights_of_a_prompt(nq, sink):
+    """One key of weight near 1 and 3999 of 2^-18 to 2^-22 of it, which make up to 1.5% of the sum."""
+    nk, d = 4000, 64
+    q, k, v = (torch.zeros(n, 1, d, dtype=FP, device="cuda") for n in (nq, nk, nk))
+    q[:, 0, 0] = 12.5 + 2.75 * torch.arange(nq, device="cuda") / nq
+    k[sink, 0, 0] = 1.0
+    v[:] = 1.0
+    v[sink] = 0.0
+    O, _ = ig.prompt_attention(q, k, v, cu([nq]), cu([nk]), causal=False, softmax_scale=1.0)
+    x = q[:, 0].double() @ k[:, 0].double().t()
+    tail_check(O[:, 0], x, v[:, 0].double(), d * 2.0 ** -23 * x.abs().amax(1))
+
+
+@pytest.mark.parametrize("B,P,n", [(1, 0, 4000), (3, 1500, 2500), (2, 4000, 0), (60, 4000, 3)])
+def test_fp16_small_weights_of_a_step(B, P, n):
+    Hq, d = 8, 64
+    q = torch.zeros(B, Hq, d, dtype=FP, device="cuda")
+    q[..., 0] = 12.5 + 2.75 * torch.arange(B * Hq, device="cuda").view(B, Hq) / (B * Hq)
+    k, v = torch.zeros(1, P + n, d, dtype=FP, device="cuda"), torch.ones(1, P + n, d, dtype=FP, device="cuda")
+    k[0, 77, 0], v[0, 77] = 1.0, 0.0
+    kc, vc = (t[:, P:].expand(B, 1, n, d).contiguous() for t in (k, v))
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    O, _ = ig.prefix_attention(q, k[:, :P].contiguous(), v[:, :P].contiguous(), kc, vc, lens, softmax_scale=1.0)
+    x = q.flatten(0, 1).double() @ k[0].double().t()
+    tail_check(O.flatten(0, 1), x, v[0].double(), d * 2.0 ** -23 * x.abs().amax(1))
+
+
 # ----------------------------------------------------------------- refusals
 def test_binding_refusals():
     q, k = normal(1, 8, 4, 64), normal(2, 8, 2, 64)
