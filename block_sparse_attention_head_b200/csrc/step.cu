@@ -161,9 +161,11 @@ __global__ void __launch_bounds__(kRowsThreads, kLong ? 2 : 3)
 
   if (warp == 4) {
     // ================================================================ loader
+    int issued = 0;
     for (int i = 0; i < nt; ++i) {
       const int st = i % L::kStages;
       if (i >= L::kStages && !mbar_wait_warp(&empty[st], (i / L::kStages - 1) & 1, abort_flag)) break;
+      issued = i + 1;
       if (lane == 0) {
         const uint32_t dst = ring + st * 2 * L::kTileBytes;
         mbar_arrive_expect_tx(&full[st], 2 * L::kTileBytes);
@@ -174,8 +176,8 @@ __global__ void __launch_bounds__(kRowsThreads, kLong ? 2 : 3)
                       (t0 + i) * kRowsKeys, z, &full[st]);
       }
     }
-    for (int i = max(0, nt - L::kStages); i < nt; ++i)  // no copy in flight is left behind
-      if (!mbar_wait_warp(&full[i % L::kStages], (i / L::kStages) & 1, abort_flag)) break;
+    for (int i = max(0, issued - L::kStages); i < issued; ++i)  // no copy in flight is left behind
+      mbar_wait_drain(&full[i % L::kStages], (i / L::kStages) & 1);
     return;
   }
 
