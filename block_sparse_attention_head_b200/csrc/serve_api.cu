@@ -60,6 +60,9 @@ int prompt_args(const instagen_prompt_params* p, ig::PromptArgs* a) {
   return IG_OK;
 }
 
+// fp32 buffers are read and written element by element
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 // (need = 256: the call uses none)
 bool good_ws(const void* ws, size_t have, size_t need) {
   if (need == 256 && !ws) return true;
@@ -119,7 +122,7 @@ int instagen_prompt_attention(const void* Q, const void* K, const void* V, const
     return IG_ERR_INVALID_ARG;
   if (p->Tq == 0) return IG_OK;
   if (!Q || !O || !cu_q || !cu_k || (p->Tk > 0 && (!K || !V))) return IG_ERR_INVALID_ARG;
-  if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(O) || !aligned16(lse)) return IG_ERR_INVALID_ARG;
+  if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(O) || !aligned4(lse)) return IG_ERR_INVALID_ARG;
   if (!good_ws(ws, ws_bytes, ig::prompt_attention_ws(a))) return IG_ERR_WORKSPACE;
   a.Q = Q;
   a.K = K;
@@ -144,7 +147,7 @@ int instagen_key_weights(const void* Q, const void* K, const float* lse, const i
   if (rc) return rc;
   if (p->Tq == 0 || p->Tk == 0) return IG_OK;
   if (!Q || !K || !lse || !cu_q || !cu_k || !weights) return IG_ERR_INVALID_ARG;
-  if (!aligned16(Q) || !aligned16(K) || !aligned16(lse) || !aligned16(weights)) return IG_ERR_INVALID_ARG;
+  if (!aligned16(Q) || !aligned16(K) || !aligned4(lse) || !aligned4(weights)) return IG_ERR_INVALID_ARG;
   if (!good_ws(ws, ws_bytes, ig::key_weights_ws(a))) return IG_ERR_WORKSPACE;
   a.Q = Q;
   a.K = K;
@@ -169,7 +172,7 @@ int instagen_prefix_attention(const void* Q, const void* Kp, const void* Vp, con
   if (rc) return rc;
   if (!Q || !O || !lens || (p->P > 0 && (!Kp || !Vp)) || (p->cap > 0 && (!Kc || !Vc))) return IG_ERR_INVALID_ARG;
   if (!aligned16(Q) || !aligned16(Kp) || !aligned16(Vp) || !aligned16(Kc) || !aligned16(Vc) || !aligned16(O) ||
-      !aligned16(lse) || !aligned16(weights))
+      !aligned4(lse) || !aligned4(weights))
     return IG_ERR_INVALID_ARG;
   if (!good_ws(ws, ws_bytes, ig::step_ws(a, weights != nullptr))) return IG_ERR_WORKSPACE;
   a.Q = Q;

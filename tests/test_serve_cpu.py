@@ -170,3 +170,16 @@ def test_every_valid_prompt_has_a_workspace_size(lib, Tk, kw):
     p = prompt(nseq=1, Hq=8, Hkv=8, **{"Tk": Tk, "Tq": 4, **kw})
     assert lib.instagen_prompt_attention_workspace_size(ctypes.byref(p)) >= 256
     assert lib.instagen_key_weights_workspace_size(ctypes.byref(p)) >= 256
+
+
+def test_fp32_buffers_may_start_at_any_element(lib):
+    """lse and weights: a layer of a larger buffer.  (The workspace is refused
+    here, after every pointer has been accepted.)"""
+    four, two = ctypes.c_void_p((1 << 20) + 4), ctypes.c_void_p((1 << 20) + 2)
+    split = prompt(nseq=1, Tq=4, Tk=100000)
+    for lse, code in ((four, WORKSPACE), (two, INVALID)):
+        assert lib.instagen_prompt_attention(*[FAKE] * 5, ctypes.byref(split), FAKE, lse, FAKE, 16, None) == code
+        assert lib.instagen_key_weights(FAKE, FAKE, lse, FAKE, FAKE, ctypes.byref(prompt()), FAKE, FAKE, 16, None) == code
+        assert lib.instagen_key_weights(FAKE, FAKE, FAKE, FAKE, FAKE, ctypes.byref(prompt()), lse, FAKE, 16, None) == code
+        for a in ((lse, None), (None, lse), (lse, lse)):
+            assert lib.instagen_prefix_attention(*[FAKE] * 6, ctypes.byref(cache()), FAKE, *a, FAKE, 16, None) == code

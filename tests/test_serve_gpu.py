@@ -744,6 +744,22 @@ def test_fp16_small_weights_of_a_step(B, P, n):
     tail_check(O.flatten(0, 1), x, v[0].double(), d * 2.0 ** -23 * x.abs().amax(1))
 
 
+def test_one_layer_of_odd_sized_lse_and_weights():
+    qs, Hq, Hkv, d = [33, 20], 3, 1, 64
+    q, k, v = normal(1, 53, Hq, d), normal(2, 53, Hkv, d), normal(3, 53, Hkv, d)
+    lse, w = torch.zeros(3, Hq, 53, device="cuda"), torch.zeros(3, Hkv, 53, device="cuda")
+    O, _ = ig.prompt_attention(q, k, v, cu(qs), cu(qs), lse=lse[1])
+    ig.key_weights(q, k, lse[1], cu(qs), cu(qs), w[1])
+    check_prompt(q, k, v, qs, qs, True, O, lse[1], weights=w[1], before=torch.zeros(Hkv, 53, device="cuda"))
+    s = step_inputs("odd", BF)
+    B, Hkv, cap = s[3].shape[:3]
+    lse, w = torch.zeros(3, B, s[0].shape[1], device="cuda"), torch.zeros(3, B, Hkv, cap, device="cuda")
+    O, _ = ig.prefix_attention(*s, lse=lse[1], weights=w[1])
+    check_step(*s, O, lse[1], torch.zeros_like(w[1]), w[1])
+    assert (lse[0] == 0).all() and (lse[2] == 0).all() and (w[0] == 0).all() and (w[2] == 0).all()
+    ig.device_status()
+
+
 # ----------------------------------------------------------------- refusals
 def test_binding_refusals():
     q, k = normal(1, 8, 4, 64), normal(2, 8, 2, 64)
