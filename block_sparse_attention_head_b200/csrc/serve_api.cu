@@ -204,7 +204,8 @@ int instagen_evict(const void* K, const void* V, const float* weights, const int
   if (rc) return rc;
   if (budget < 1 || recent < 0 || budget > cap_out) return IG_ERR_INVALID_ARG;
   if ((long long)c.B * c.Hkv * cap_out > 2147483647LL - 1024) return IG_ERR_UNSUPPORTED;
-  if (!K || !V || !weights || !pos || !lens || !K_out || !V_out || !weights_out || !pos_out || !lens_out)
+  if ((c.cap > 0 && (!K || !V || !weights || !pos)) || !lens || !K_out || !V_out || !weights_out || !pos_out ||
+      !lens_out)
     return IG_ERR_INVALID_ARG;
   if (!aligned16(K) || !aligned16(V) || !aligned16(K_out) || !aligned16(V_out)) return IG_ERR_INVALID_ARG;
   const int same = (K == K_out) + (V == V_out) + (weights == weights_out) + (pos == pos_out) + (lens == lens_out);

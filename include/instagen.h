@@ -458,7 +458,8 @@ int instagen_prefix_attention(const void* Q, const void* Kp, const void* Vp, con
  * written by the same call and few rows move when few are evicted; a slot's
  * position is what pos says, not its index.
  *   K, V [B, Hkv, cap, d], weights [B, Hkv, cap] fp32, pos [B, Hkv, cap] int32
- *   (token positions), lens [B] int32 (clamped as above).
+ *   (token positions), lens [B] int32 (clamped as above); the first four may
+ *   be NULL when cap = 0.
  *   Outputs: all five pointers equal to the inputs and cap_out = cap (in
  *   place: only the moving rows are touched), or all five distinct buffers
  *   with cap_out slots per head (the kept rows are copied; a large prompt

@@ -183,3 +183,16 @@ def test_fp32_buffers_may_start_at_any_element(lib):
         assert lib.instagen_key_weights(FAKE, FAKE, FAKE, FAKE, FAKE, ctypes.byref(prompt()), lse, FAKE, 16, None) == code
         for a in ((lse, None), (None, lse), (lse, lse)):
             assert lib.instagen_prefix_attention(*[FAKE] * 6, ctypes.byref(cache()), FAKE, *a, FAKE, 16, None) == code
+
+
+def test_evict_takes_caches_without_slots(lib):
+    p = cache(P=0, prefix_head=0, cap=0)
+    need = lib.instagen_evict_workspace_size(ctypes.byref(p), 20)
+    out = [ctypes.c_void_p((2 + i) << 20) for i in range(5)]
+
+    def call(ins, outs=out, n=need - 1):
+        return lib.instagen_evict(*ins, ctypes.byref(p), 20, 4, *outs, 30, FAKE, n, None)
+
+    assert need > 0 and call([None] * 4 + [FAKE]) == WORKSPACE  # (only that is refused)
+    assert call([None] * 5) == INVALID                          # lens is read
+    assert call([None] * 4 + [FAKE], outs=[None] + out[1:]) == INVALID

@@ -760,6 +760,16 @@ def test_one_layer_of_odd_sized_lse_and_weights():
     ig.device_status()
 
 
+def test_evict_caches_without_slots():
+    B, Hkv, d = 3, 2, 64
+    t = evict_inputs(B, Hkv, 0, d, [0] * B, "spread")
+    out = tuple(torch.full((B, Hkv, 5, *x.shape[3:]), 9, dtype=x.dtype, device="cuda") for x in t[:4]) + (
+        torch.full((B,), 9, dtype=torch.int32, device="cuda"),)
+    got = ig.evict(*t, 5, 1, out=out)
+    assert (got[4] == 0).all() and all((x == 9).all() for x in got[:4])
+    ig.device_status()
+
+
 # ----------------------------------------------------------------- refusals
 def test_binding_refusals():
     q, k = normal(1, 8, 4, 64), normal(2, 8, 2, 64)
