@@ -770,6 +770,75 @@ def test_evict_caches_without_slots():
     ig.device_status()
 
 
+# -------------------------------------- forms that only some sizes reach
+def check_evict_long(before, after, budget, recent):
+    """check_evict for one long cache, by sorting."""
+    k, v, w, pos, lens = before
+    n = int(lens[0])
+    x, t = w[0, 0, :n].double().cpu().numpy(), pos[0, 0, :n].cpu().numpy().astype(np.int64)
+    nan = np.isnan(x)
+    order = np.lexsort((np.arange(n), -np.where(nan, 0.0, x), nan, ~(t > t.max() - recent)))
+    kept = np.sort(order[:budget])
+    source = np.arange(budget)
+    stays = np.zeros(budget, dtype=bool)
+    stays[kept[kept < budget]] = True
+    source[~stays] = kept[kept >= budget]
+    at = torch.tensor(source, device="cuda")
+    assert int(after[4][0]) == budget
+    for got, ref in zip(after[:4], before[:4]):
+        assert torch.equal(torch.nan_to_num(got[0, 0, :budget].float()), torch.nan_to_num(ref[0, 0, at].float()))
+
+
+@pytest.mark.parametrize("place", [True, False], ids=["in_place", "copy"])
+@pytest.mark.parametrize("kind", ["ties", "odd"])
+@pytest.mark.parametrize("cap,n,budget,recent", [
+    (420000, 419999, 100000, 1000),  # a CTA's part of 52512 slots: read again in every pass
+    (420000, 300001, 70, 100),
+    (80003, 80000, 40000, 7),        # parts of 10016 slots: more than a thread's registers hold
+], ids=["unheld", "unheld_recent", "held"])
+def test_evict_long_parts(cap, n, budget, recent, kind, place):
+    t = evict_inputs(1, 1, cap, 64, [n], kind)
+    before = [x.clone() for x in t]
+    out = None if place else tuple(
+        torch.zeros(1, 1, budget, *x.shape[3:], dtype=x.dtype, device="cuda") for x in t[:4]) + (t[4].clone(),)
+    check_evict_long(before, ig.evict(*t, budget, recent, out=out), budget, recent)
+    ig.device_status()
+
+
+@pytest.mark.parametrize("kind", ["ties", "odd"])
+@pytest.mark.parametrize("Hkv,cap,n", [(2, 2050, 2049), (2, 4000, 3999), (1, 6001, 6000), (80, 5000, 4900)])
+def test_evict_clusters_of_two_and_four(Hkv, cap, n, kind):
+    t = evict_inputs(1, Hkv, cap, 64, [n], kind)
+    before = [x.clone() for x in t]
+    check_evict(before, ig.evict(*t, n // 3, 100), n // 3, 100)
+    ig.device_status()
+
+
+@pytest.mark.parametrize("keep", [False, True], ids=["plain", "weights"])
+@pytest.mark.parametrize("B,P,lens,cap", [(1, 0, [49000], 50000), (1, 17000, [49000], 50000), (1, 40000, [0], 0),
+                                          (2, 300, [66000, 40000], 66000)])
+def test_steps_with_more_than_32_parts(B, P, lens, cap, keep):
+    Hq, Hkv, d = 4, 1, 64
+    q, kp, vp = normal(1, B, Hq, d, scale=1.2), normal(2, Hkv, P, d, scale=1.2), normal(3, Hkv, P, d)
+    kc, vc = normal(4, B, Hkv, cap, d, scale=1.2), normal(5, B, Hkv, cap, d)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    before = normal(6, B, Hkv, cap, dtype=torch.float32).abs()
+    w = before.clone() if keep else None
+    O, lse = ig.prefix_attention(q, kp, vp, kc, vc, n, weights=w)
+    check_step(q, kp, vp, kc, vc, n, O, lse, before, w)
+    ig.device_status()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_one_long_prompt_among_short_ones(d):
+    qs, ks = [1 + i % 5 for i in range(30)] + [700, 2], [3 + i % 7 for i in range(30)] + [6000, 2]
+    q, k, v = normal(1, sum(qs), 4, d, scale=1.2), normal(2, sum(ks), 2, d, scale=1.2), normal(3, sum(ks), 2, d)
+    O, lse = ig.prompt_attention(q, k, v, cu(qs), cu(ks))
+    w = ig.key_weights(q, k, lse, cu(qs), cu(ks), torch.zeros(2, sum(ks), device="cuda"))
+    check_prompt(q, k, v, qs, ks, True, O, lse, weights=w, before=torch.zeros_like(w))
+    ig.device_status()
+
+
 # ----------------------------------------------------------------- refusals
 def test_binding_refusals():
     q, k = normal(1, 8, 4, 64), normal(2, 8, 2, 64)
