@@ -13,6 +13,7 @@ half a step of the 16-bit type (2^-8 bf16, 2^-11 fp16),
             of the sum for adding it up in fp32
 """
 import math
+import os
 import threading
 
 import numpy as np
@@ -836,6 +837,35 @@ def test_one_long_prompt_among_short_ones(d):
     O, lse = ig.prompt_attention(q, k, v, cu(qs), cu(ks))
     w = ig.key_weights(q, k, lse, cu(qs), cu(ks), torch.zeros(2, sum(ks), device="cuda"))
     check_prompt(q, k, v, qs, ks, True, O, lse, weights=w, before=torch.zeros_like(w))
+    ig.device_status()
+
+
+def test_the_readme_example():
+    """The language-model example of README.md, each step against its definition."""
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
+    code = text.split("```python\n")[1].split("```")[0]
+    qs, Hq, Hkv, d = [1500, 40, 1100], 4, 2, 64
+    B, T, c = len(qs), sum(qs), cu(qs)
+    q, k, v = normal(1, T, Hq, d), normal(2, T, Hkv, d), normal(3, T, Hkv, d)
+    env = dict(q=q, k=k, v=v, cu=c, B=B, T=T, Hq=Hq, Hkv=Hkv, d=d, q1=normal(4, B, Hq, d),
+               k_shared=normal(5, Hkv, 300, d), v_shared=normal(6, Hkv, 300, d))
+    head, tail = code.split("# keep 1024 keys")
+    exec(head, env)
+    check_prompt(q, k, v, qs, qs, True, env["o"], env["lse"], weights=env["w"], before=torch.zeros(Hkv, T, device="cuda"))
+    start = 0
+    for b, n in enumerate(qs):
+        assert torch.equal(env["kc"][b, :, :n], k[start:start + n].transpose(0, 1))
+        assert torch.equal(env["vc"][b, :, :n], v[start:start + n].transpose(0, 1))
+        assert torch.equal(env["wc"][b, :, :n], env["w"][:, start:start + n])
+        start += n
+    before = [env[n] for n in ("kc", "vc", "wc", "pos", "lens")]
+    exec("# keep 1024 keys" + tail.split("# one token")[0], env)
+    after = [env[n] for n in ("kc", "vc", "wc", "pos", "lens")]
+    check_evict(before, after, 1024, 128)
+    weights = env["wc"].clone()
+    exec("# one token" + tail.split("# one token")[1], env)
+    check_step(env["q1"], env["k_shared"], env["v_shared"], after[0], after[1], after[4], env["o"], env["lse"], weights,
+               env["wc"])
     ig.device_status()
 
 
