@@ -12,8 +12,8 @@
 // reads 128, all there is.  Three score tiles of 128 columns rotate between
 // the MMA warp and four warpgroups, each of which takes every fourth one:
 // product, load and exponentials of three visits overlap.  (Two warpgroups with
-// twice the registers and a whole row in them: 387 us for 2048 queries on 16384
-// keys, 32/4 heads, d = 128, against 356.)  lse comes through
+// twice the registers and a whole row in them took 9% longer for 2048 queries on
+// 16384 keys, 32/4 heads, d = 128, which take 370 us now.)  lse comes through
 // shared memory, converted once per tile to its negative in log2 units (-inf
 // for rows that see nothing or do not exist).
 //
@@ -331,7 +331,10 @@ __global__ void __launch_bounds__(256) add_parts_kernel(KwArgs a) {
 
 // CTAs per key pair: the visits of a pair are split where that shortens the
 // whole: waves of CTAs times a CTA's visits and the 6 that its start and end
-// cost, in parts of at least 4 visits.
+// cost, in parts of at least 4 visits.  Measured (bf16, d = 128, causal) with 0, 3,
+// 6, 12 for them: 2048 queries on 16384 keys, 32/4 heads 664, 373, 369, 370 us; 6 x
+// up to 1000, 32/8 76, 57, 49, 56; 4 x up to 512, 32/8 26.5, 26.5, 32.8, 32.8; 8192,
+// 8/8 277, 102, 102, 102; 256 on 8192, 64 on 30000, 16 x 300 and 3 x 100: the same.
 static int key_weight_splits(const PromptArgs& a) {
   const long long ctas = row_pairs(a.Tk, 1, a.nseq) * a.Hkv;
   const long long visits = (long long)a.G * ((a.Tq / a.nseq + kKwTile - 1) / kKwTile);

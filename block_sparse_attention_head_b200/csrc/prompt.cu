@@ -834,8 +834,10 @@ cudaError_t launch_prompt_attention(const PromptArgs& p, cudaStream_t s) {
   a.nsplit = prompt_splits(p);
   // Long keys and few units: the sequences' last pairs, where they hold one row
   // tile (half the time), start last and fill the end.  4 chunks of 257 rows
-  // on up to 8191 keys, 40 heads: 268 us against 280.  Each costs an idle CTA
-  // of a microsecond, so not with many short sequences.
+  // on up to 8191 keys, 40 heads, bf16: 268 us against 274 to 281; 2 of 1100 on
+  // up to 6000, 16 heads: 110.6 against 113.8; 4 of 300 on 4096, 4 of 385 on 8191
+  // and 8 of 100 on 3000: the same.  Each costs an idle CTA of a microsecond, so
+  // not with many short sequences.
   if (a.nsplit == 1 && p.nseq * p.Hkv <= 2 * kSms && p.Tk / p.nseq >= 2048) {
     a.short_last = a.ntile;
     a.ntile += p.nseq;

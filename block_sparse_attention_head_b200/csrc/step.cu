@@ -19,8 +19,9 @@
 // The launches overlap (neither of the two reads what the other writes), and
 // finish_kernel's CTAs wait where they need the parts.  The prefix goes first
 // where it leaves SMs for all of the caches' CTAs (32 sequences behind 4000
-// keys: 25 us against 33); else the caches do, and the prefix's CTAs take the
-// SMs as they come free (128 sequences behind 32768 keys: 102 us against 110).
+// keys, with weights: 29.7 us against 35.8); else the caches do, and the prefix's
+// CTAs take the SMs as they come free (8 sequences with 3000 keys of their own
+// behind 30000: 60 us against 73; 128 with 200 behind 32768: 108.6 against 111.6).
 #include "serve.cuh"
 
 namespace ig {

@@ -368,7 +368,9 @@ int instagen_forward_layout_get(const instagen_params* p, instagen_forward_layou
  * row with a NaN logit are NaN.  A logit of -inf (dots may overflow) weighs 0;
  * a weight below 2^-126 of its row's largest may count as less, down to 0.
  * Results do not depend on timing: no atomics on floats.  Pointers to 16-bit
- * tensors must be 16-byte aligned (fp32 and int32 buffers 4-byte).
+ * tensors must be 16-byte aligned (fp32 and int32 buffers 4-byte).  Where a wait
+ * timed out (IG_ERR_DEVICE_CHECK), what the call writes is undefined, weights
+ * included: start again from weights that were saved, or from zeros.
  * Workspaces are scratch: 256-byte aligned, no contents kept; calls that may
  * overlap on the GPU (two streams, two captured graphs) need one each.  A
  * size function returns 0 for invalid parameters and at least 256 otherwise;
